@@ -1,9 +1,9 @@
 """GB300 prompt-lookup (n-gram) speculative drafting.
 
 Python binding of the C ABI in ``include/lookup_draft.h``,
-``include/lookup_loop.h``, ``include/lookup_index.h`` and
-``include/lookup_ctxcache.h`` (ctypes; argument marshalling only -- every step
-runs in the library's CUDA kernels).
+``include/lookup_loop.h``, ``include/lookup_index.h``,
+``include/lookup_ctxcache.h`` and ``include/lookup_target.h`` (ctypes; argument
+marshalling only -- every step runs in the library's CUDA kernels).
 PyTorch tensors supply device memory and the current CUDA stream.
 
     draft, length, pos = lookup_draft(tokens, offsets, min_m=4, max_m=12, K=15)
@@ -32,6 +32,7 @@ __all__ = [
     "NgramIndex", "index_slots_for", "index_bytes", "lookup_index_build", "lookup_index_append",
     "lookup_index_draft", "lookup_index_draft_plan", "lookup_index_verify_append",
     "lookup_index_verify_append_draft", "ContextCache",
+    "lookup_kv_append", "lookup_paged_attention", "lookup_verify_logits", "rotary_table", "PagedKVCache",
     "load_checked_library", "check_word",
     "launch_count",
     "MAX_M", "MAX_K", "LEN_FAILED", "CHECK_BITS",
@@ -172,7 +173,7 @@ def _declare_draft(lib: ctypes.CDLL) -> None:
 
 def _declare_loop(lib: ctypes.CDLL) -> None:
     """Argument types of the entry points in include/lookup_loop.h,
-    include/lookup_index.h and include/lookup_ctxcache.h."""
+    include/lookup_index.h, include/lookup_ctxcache.h and include/lookup_target.h."""
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     lib.lookup_fuse.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp, vp, vp]
     lib.lookup_fuse.restype = ctypes.c_int
@@ -218,6 +219,16 @@ def _declare_loop(lib: ctypes.CDLL) -> None:
     lib.lookup_ctx_append.restype = ctypes.c_int
     lib.lookup_ctx_draft.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i64, vp, vp, vp]
     lib.lookup_ctx_draft.restype = ctypes.c_int
+    lib.lookup_kv_append.argtypes = [vp] * 9 + [i32] * 8 + [vp] + [i32] * 4 + [vp] * 5
+    lib.lookup_kv_append.restype = ctypes.c_int
+    lib.lookup_paged_attention_workspace_bytes.argtypes = [i32] * 5
+    lib.lookup_paged_attention_workspace_bytes.restype = sz
+    lib.lookup_paged_attention.argtypes = [vp] * 7 + [i32] * 8 + [f32, i32, i32, vp, vp, vp, sz, vp]
+    lib.lookup_paged_attention.restype = ctypes.c_int
+    lib.lookup_verify_logits_workspace_bytes.argtypes = [i32] * 3
+    lib.lookup_verify_logits_workspace_bytes.restype = sz
+    lib.lookup_verify_logits.argtypes = [vp] * 4 + [i32] * 2 + [vp] * 6 + [i32] * 2 + [vp] * 5 + [sz, vp]
+    lib.lookup_verify_logits.restype = ctypes.c_int
 
 
 def _check(rc: int, lib) -> None:
@@ -922,3 +933,241 @@ class ContextCache:
                                       self.slots, dp, lnp, _stream_handle(stream))
         _check(rc, lib)
         return d, ln
+
+
+# ------------------------------------------- the target's side of a verify step ----
+_TYPES = {"float32": 0, "float16": 1, "bfloat16": 2}      # LOOKUP_TYPE_* of include/lookup_target.h
+
+
+def _type_code(t, name, allowed):
+    code = _TYPES.get(str(t.dtype).removeprefix("torch."))
+    if code is None or code not in allowed:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return code
+
+
+def _strided(t, shape, dtype, device, name):
+    """Check a device tensor whose last axis is dense and whose other strides are free;
+    return its pointer and the C array of those strides."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: the last axis must be dense")
+    if any(x < 0 for x in st):
+        raise ValueError(f"{name}: negative strides")
+    return t.data_ptr(), (ctypes.c_int64 * (len(shape) - 1))(*st[:-1])
+
+
+def _cuda_device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _scratch(nbytes, workspace, device, stream):
+    """The call's workspace: the caller's, or one from PyTorch's allocator that stays
+    reserved until the stream is past the call."""
+    import torch
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return workspace, workspace.numel() * workspace.element_size()
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws, nbytes
+
+
+def rotary_table(max_pos: int, rot: int, base: float = 10000.0, scaling=None, device=None):
+    """The table lookup_kv_append rotates with: float32 [max_pos, rot], for each position
+    rot/2 cosines and rot/2 sines.  The angles p * base**(-2i/rot) are formed in 64
+    bits, so positions past 2**17 keep their fraction of a turn.
+
+    ``scaling`` for contexts longer than the model was trained on:
+      ("linear", factor)         every angle divided by factor
+      ("base", factor)           base grown to base * factor**(rot / (rot - 2)): the
+                                 slowest angle divided by factor, the fastest kept
+      ("bands", factor, original, fast, slow[, amplitude])
+                                 an angle that turns more than ``fast`` times over
+                                 ``original`` positions is kept, one that turns less
+                                 than ``slow`` times is divided by factor, a ramp
+                                 linear in the angle's index between; cosines and
+                                 sines times amplitude
+                                 (default 0.1 * ln(factor) + 1)
+    """
+    import math
+
+    import torch
+    if max_pos < 1 or rot < 2 or rot % 2 or not base > 0:
+        raise ValueError("rotary_table needs max_pos >= 1, an even rot >= 2 and a positive base")
+    half, amplitude = rot // 2, 1.0
+    kind = scaling[0] if scaling is not None else None
+    if kind == "base":
+        if rot < 4:
+            raise ValueError('scaling "base" needs rot >= 4')
+        base = base * float(scaling[1]) ** (rot / (rot - 2))
+    freq = base ** (-torch.arange(half, dtype=torch.float64) / half)
+    if kind == "linear":
+        freq = freq / float(scaling[1])
+    elif kind == "bands":
+        factor, original, fast, slow = (float(x) for x in scaling[1:5])
+        if not (factor >= 1 and original >= 1 and fast > slow > 0):
+            raise ValueError('scaling "bands" needs factor >= 1, original >= 1 and fast > slow > 0')
+
+        def index_of(turns):         # the (fractional) index of the angle with that many turns
+            return half * math.log(original / (2 * math.pi * turns)) / math.log(base)
+
+        first, last = max(math.floor(index_of(fast)), 0), min(math.ceil(index_of(slow)), half - 1)
+        ramp = ((torch.arange(half, dtype=torch.float64) - first) / max(last - first, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - ramp) + freq / factor * ramp
+        amplitude = float(scaling[5]) if len(scaling) > 5 else 0.1 * math.log(factor) + 1.0
+    elif kind not in (None, "base"):
+        raise ValueError(f"unknown scaling {kind!r}")
+    ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq
+    table = torch.cat([ang.cos(), ang.sin()], 1) * amplitude
+    return table.to(torch.float32).to(device if device is not None else "cuda").contiguous()
+
+
+def _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, dtype, dev):
+    """Check the paged cache's tensors; returns (pages, Hkv, page_size, max_pages, pointers)."""
+    import torch
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache must be [pages, Hkv, page_size, D] and block_table [B, max_pages]")
+    pages, hkv, page, _ = k_cache.shape
+    mp = block_table.shape[1]
+    shape = (pages, hkv, page, D)
+    ptrs = (_dev(k_cache, dtype, shape, dev, "k_cache"), _dev(v_cache, dtype, shape, dev, "v_cache"),
+            _dev(block_table, torch.int32, (B, mp), dev, "block_table"),
+            _dev(kv_len, torch.int32, (B,), dev, "kv_len"), _dev(q_len, torch.int32, (B,), dev, "q_len", optional=True))
+    return pages, hkv, page, mp, ptrs
+
+
+def lookup_kv_append(q, k, v, kv_len, block_table, k_cache, v_cache, rotary=None, rot=None, q_len=None,
+                     interleaved: bool = False, out_q=None, status=None, stream=None):
+    """Rotate a verify block's queries and keys and write its keys and values to the paged
+    cache [pages, Hkv, page_size, D] (include/lookup_target.h).  q [B, N, Hq, D], k and
+    v [B, N, Hkv, D] may be strided views; ``rotary`` is rotary_table's [max_pos, rot].
+    Returns (rotated q [B, N, Hq, D], status [B]: 1 where a token had no slot)."""
+    import torch
+    lib = load_library()
+    dev = _cuda_device(q, "q")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, N, heads, D]")
+    B, N, hq, D = q.shape
+    code = _type_code(q, "q", (1, 2))
+    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, q.dtype, dev)
+    qp, qs = _strided(q, (B, N, hq, D), q.dtype, dev, "q")
+    kp, ks = _strided(k, (B, N, hkv, D), q.dtype, dev, "k")
+    vp, vs = _strided(v, (B, N, hkv, D), q.dtype, dev, "v")
+    rp, max_pos = None, 0
+    if rotary is not None:
+        if rotary.dim() != 2:
+            raise ValueError("rotary must be [max_pos, rot]")
+        max_pos, width = rotary.shape
+        if rot is not None and rot != width:
+            raise ValueError("rot differs from the table's width")
+        rot = width
+        rp = _dev(rotary, torch.float32, (max_pos, width), dev, "rotary")
+    if out_q is None:
+        out_q = torch.empty((B, N, hq, D), dtype=q.dtype, device=dev)
+    if status is None:
+        status = torch.empty(B, dtype=torch.int32, device=dev)
+    if N == 0:
+        status.zero_()
+    op = _dev(out_q, q.dtype, (B, N, hq, D), dev, "out_q")
+    sp = _dev(status, torch.int32, (B,), dev, "status")
+    with torch.cuda.device(dev):
+        rc = lib.lookup_kv_append(qp, qs, kp, ks, vp, vs, kl, ql, bt, B, N, hq, hkv, D, mp, pages, page, rp, rot or 0,
+                                  max_pos, 1 if interleaved else 0, code, kc, vc, op, sp, _stream_handle(stream))
+    _check(rc, lib)
+    return out_q, status
+
+
+def lookup_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=None, window: int = 0,
+                           out=None, lse=None, workspace=None, stream=None):
+    """Attention of the block's tokens over the paged cache that already holds them
+    (include/lookup_target.h): q [B, N, Hq, D], token i of request r at position
+    kv_len[r] + i.  ``scale`` defaults to D**-0.5; ``window`` > 0 limits each token to
+    itself and the window - 1 before it.  Returns (out [B, N, Hq, D], lse float32 [B, N, Hq])."""
+    import torch
+    lib = load_library()
+    dev = _cuda_device(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, D]")
+    B, N, hq, D = q.shape
+    code = _type_code(q, "q", (1, 2))
+    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, q.dtype, dev)
+    qp, qs = _strided(q, (B, N, hq, D), q.dtype, dev, "q")
+    if out is None:
+        out = torch.empty((B, N, hq, D), dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((B, N, hq), dtype=torch.float32, device=dev)
+    op = _dev(out, q.dtype, (B, N, hq, D), dev, "out")
+    lp = _dev(lse, torch.float32, (B, N, hq), dev, "lse")
+    with torch.cuda.device(dev):
+        ws, nbytes = _scratch(lib.lookup_paged_attention_workspace_bytes(B, N, hq, hkv, D), workspace, dev, stream)
+        rc = lib.lookup_paged_attention(qp, qs, kc, vc, bt, kl, ql, B, N, hq, hkv, D, mp, pages, page,
+                                        D ** -0.5 if scale is None else scale, window, code, op, lp, ws.data_ptr(),
+                                        nbytes, _stream_handle(stream))
+    _check(rc, lib)
+    return out, lse
+
+
+def lookup_verify_logits(block, length, logits, noise=None, u=None, temperature=None, qprobs=None, point_mass=None,
+                         out=None, workspace=None, stream=None):
+    """Verify proposal blocks [B, P] against the target's logits [B, P + 1, V] (float32,
+    float16 or bfloat16, rows may be strided), include/lookup_target.h.  Without ``noise``
+    greedy; with it (float32 [B, V], exponential draws) sampled, with uniform draws
+    ``u`` [B, P], per-request ``temperature`` (0 = greedy) and the proposal
+    distributions ``qprobs`` [B, P, V] (None = point masses).  Returns (accepted [B],
+    commit [B, P + 1], ncommit [B], logprobs float32 [B, P + 1])."""
+    import torch
+    lib = load_library()
+    dev = _cuda_device(logits, "logits")
+    if block.dim() != 2 or logits.dim() != 3:
+        raise ValueError("block must be [B, P] and logits [B, P + 1, V]")
+    B, P = block.shape
+    V = logits.shape[2]
+    i32, f32 = torch.int32, torch.float32
+    code = _type_code(logits, "logits", (0, 1, 2))
+    lp, ls = _strided(logits, (B, P + 1, V), logits.dtype, dev, "logits")
+    qp, qs = (None, None) if qprobs is None else _strided(qprobs, (B, P, V), f32, dev, "qprobs")
+    args = (_dev(noise, f32, (B, V), dev, "noise", optional=True),
+            _dev(temperature, f32, (B,), dev, "temperature", optional=True),
+            _dev(u, f32, (B, P), dev, "u", optional=noise is None))
+    bp, np_ = _dev(block, i32, (B, P), dev, "block"), _dev(length, i32, (B,), dev, "len")
+    pm = _dev(point_mass, i32, (B, P), dev, "point_mass", optional=True)
+    if out is None:
+        out = (torch.empty(B, dtype=i32, device=dev), torch.empty((B, P + 1), dtype=i32, device=dev),
+               torch.empty(B, dtype=i32, device=dev), torch.empty((B, P + 1), dtype=f32, device=dev))
+    acc, commit, nc, lps = out
+    optr = (_dev(acc, i32, (B,), dev, "accepted"), _dev(commit, i32, (B, P + 1), dev, "commit"),
+            _dev(nc, i32, (B,), dev, "ncommit"), _dev(lps, f32, (B, P + 1), dev, "logprobs"))
+    with torch.cuda.device(dev):
+        ws, nbytes = _scratch(lib.lookup_verify_logits_workspace_bytes(B, P, V), workspace, dev, stream)
+        rc = lib.lookup_verify_logits(bp, np_, lp, ls, code, V, *args, qp, qs, pm, B, P, *optr, ws.data_ptr(), nbytes,
+                                      _stream_handle(stream))
+    _check(rc, lib)
+    return acc, commit, nc, lps
+
+
+class PagedKVCache:
+    """One layer's paged key-value cache (include/lookup_target.h): the memory and the two
+    calls that write and read it.  Pages are handed out by the caller through
+    ``block_table``."""
+
+    def __init__(self, pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=None, device=None):
+        import torch
+        dev = device if device is not None else torch.cuda.current_device()
+        shape = (pages, kv_heads, page_size, head_dim)
+        self.k = torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
+        self.v = torch.empty_like(self.k)
+
+    def append(self, q, k, v, kv_len, block_table, **options):
+        """lookup_kv_append into this cache."""
+        return lookup_kv_append(q, k, v, kv_len, block_table, self.k, self.v, **options)
+
+    def attention(self, q, block_table, kv_len, **options):
+        """lookup_paged_attention over this cache."""
+        return lookup_paged_attention(q, self.k, self.v, block_table, kv_len, **options)

@@ -1,9 +1,11 @@
 """Compile the CUDA library in-tree for GB300 (sm_103a).
 
-The library is five translation units, ``csrc/lookup_draft.cu`` (the drafting
+The library is eight translation units, ``csrc/lookup_draft.cu`` (the drafting
 step), ``csrc/lookup_loop.cu`` (the decode-loop steps around it),
 ``csrc/lookup_index.cu`` (the incremental n-gram index),
-``csrc/lookup_ctxcache.cu`` (context-cache drafting) and ``csrc/read_floor.cu``
+``csrc/lookup_ctxcache.cu`` (context-cache drafting), ``csrc/lookup_kv_append.cu``,
+``csrc/lookup_attention.cu`` and ``csrc/lookup_logits.cu`` (the target model's side
+of a verify step) and ``csrc/read_floor.cu``
 (a measurement aid: a plain streaming read), built with nvcc into
 ``_build/liblookup_draft.so`` next to this file.  The drafting step's source is
 also compiled with LOOKUP_DRAFT_CHECKED=1 into ``_build/liblookup_draft_checked.so``:
@@ -22,9 +24,10 @@ REPO_DIR = os.path.dirname(PKG_DIR)
 INCLUDE_DIR = os.path.join(REPO_DIR, "include")
 SOURCES = [os.path.join(PKG_DIR, "csrc", f)
            for f in ("lookup_draft.cu", "lookup_loop.cu", "lookup_index.cu", "lookup_ctxcache.cu",
-                     "read_floor.cu")]
+                     "lookup_kv_append.cu", "lookup_attention.cu", "lookup_logits.cu", "read_floor.cu")]
 HEADERS = [os.path.join(INCLUDE_DIR, f)
-           for f in ("lookup_draft.h", "lookup_loop.h", "lookup_index.h", "lookup_ctxcache.h")] + \
+           for f in ("lookup_draft.h", "lookup_loop.h", "lookup_index.h", "lookup_ctxcache.h",
+                     "lookup_target.h")] + \
           [os.path.join(PKG_DIR, "csrc", "common.cuh")]
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "liblookup_draft.so")
@@ -52,7 +55,7 @@ def compile_command(out: str, extra: list[str] | None = None, checked: bool = Fa
     drafting step)."""
     sources = CHECKED_SOURCES if checked else SOURCES
     defines = ["-DLOOKUP_DRAFT_CHECKED=1"] if checked else []
-    return [nvcc_path(), *ARCH_FLAGS, "-lineinfo", "-O3", "-std=c++17",
+    return [nvcc_path(), *ARCH_FLAGS, "-lineinfo", "-O3", "-std=c++17", "--threads", "4",
             "-Xcompiler", "-fPIC,-O2", "-shared", "-cudart", "static",
             "-I", INCLUDE_DIR, *defines, "-o", out, *sources, *(extra or [])]
 
