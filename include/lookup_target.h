@@ -99,13 +99,15 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
  * exp(s_j)), out = sum_j exp(s_j - lse) v_j.  Rows past q_len[r] have out = 0 and
  * lse = -infinity.  A request's tokens past the block table's end are taken as
  * absent, and a table entry outside [0, pages) as a page of zeros; slots that no
- * token of the request sees are never used, whatever they hold.  Within the
- * block's own tokens a value that is not finite (in v_cache) may reach the rows
- * before it.
+ * token of the request sees are never used, whatever they hold.  A value in v_cache
+ * that is not finite, in a slot that some tokens of the block see and others do not
+ * (the block's own tokens, a window's edge), may reach the others.
+ * A call whose bounded waits run out on the device (lookup_draft_set_wait_limit_ns)
+ * returns NaN in every element of out and lse.
  * Errors: LOOKUP_DRAFT_EINVAL for sizes outside their ranges, a null pointer other than
  * q_len and lse, pointers or strides of q and the caches that are not multiples of 16 bytes, a
- * workspace that is too small, or caches of 2^31 rows (pages * Hkv * page_size)
- * or more.
+ * workspace that is too small, or caches (pages * Hkv * page_size) or block tables
+ * (max_pages * page_size) of 2^31 - 129 rows or more.
  */
 size_t lookup_paged_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);
 

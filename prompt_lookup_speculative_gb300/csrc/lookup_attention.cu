@@ -1,151 +1,886 @@
 // lookup_attention.cu -- attention of a verify block over the paged cache.
 //
-// The contract is in include/lookup_target.h (lookup_paged_attention).  One warp per
-// (query row, part of the cache's length), a running maximum and sum; a second
-// kernel joins the parts.
+// The contract is in include/lookup_target.h (lookup_paged_attention).
+//
+// The mathematics: out = sum_j p_j v_j / sum_j p_j with p_j = 2^(c q.k_j - c m),
+// c = |scale| log2(e) (a negative scale is folded into q, exactly), in one pass over
+// the cache with a running m per row: the sums so far are brought to a larger m by
+// one factor.  m follows the row's maximum only when that is more than 2^8 ahead:
+// p then stays within 2^8, which neither type's range nor its relative rounding
+// notices, and most tiles need no correction of the sums.
+//
+// What bounds it: the cache's bytes, read once.  The block's N tokens and the G =
+// Hq / Hkv query heads of one key-value head share every key they read, so their
+// N * G rows form the M = 128 rows of tcgen05 products (16 tokens of 8 heads fill
+// them exactly; fewer rows leave lanes idle, which costs no bytes): S = Q K^T of 128
+// rows by 64 positions into tensor memory, softmax by one thread per row, P back
+// into tensor memory over S, O += P V from there.
+//
+// Split: the work of all requests, heads and row tiles is laid end to end in units
+// of 64 positions and cut into equal contiguous ranges, one per CTA (two CTAs per
+// SM), so that neither ragged lengths nor few requests leave an SM without work.
+// A CTA finds its range from kv_len and q_len on the device.  An item that lies in
+// one range is finished there; the parts of one that is cut go to the workspace and
+// join_kernel adds them, in the order of the ranges: no atomics, the same bits every
+// time.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
 #include "common.cuh"
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
 namespace {
 
 using lkd::allow_dependent_launch;
-using lkd::launch_pdl;
+using lkd::mbar_expect_tx;
+using lkd::mbar_init;
+using lkd::mbar_try_wait;
+using lkd::smem_addr;
 using lkd::wait_for_prerequisite_grid;
 
-constexpr int kWarps = 4;
-constexpr int kMaxParts = 32;
+constexpr int kRows = 128;               // rows of a tile: M of the products, lanes of tensor memory
+constexpr int kTile = 64;                // positions of a tile
+constexpr int kSoftWarps = 4;            // one thread per row
+constexpr int kLoadWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kJoinRows = 8;             // rows a CTA of join_kernel finishes
+constexpr int kJoinThreads = 32 * kJoinRows;
+constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
+constexpr int kMaxCtas = 2 * kMaxSms;
+constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
+constexpr int kBarBytes = 1024;          // barriers and small state ahead of the tiles
 
-struct Params {
-    const void *q;
-    int64_t qb, qn, qh;
-    const void *k_cache, *v_cache;
-    const int32_t *table, *kv_len, *q_len;
-    int32_t B, N, Hq, Hkv, max_pages, pages, page_shift, window, parts;
-    float scale;
-    void *out;
-    float *lse, *ws;                     // ws: [row][parts][D + 2]: m, s, o
+// Shared memory and tensor memory of head size D.  A slot holds one tile of K or V.
+template <int D>
+struct Shape {
+    static constexpr int kCtas = D == 256 ? 1 : 2;           // per SM
+    static constexpr int kSlotBytes = kTile * D * 2;
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kSlots = D == 256 ? 5 : (112 * 1024 - kQBytes) / kSlotBytes;
+    static constexpr int kSmem = kBarBytes + kQBytes + kSlots * kSlotBytes;
+    static constexpr int kCols = D == 256 ? 512 : 256;       // tensor memory: S twice, O
+    static constexpr int kO = 2 * kTile;                     // O's first column
 };
 
-__device__ inline float to_f32(__half x) { return __half2float(x); }
-__device__ inline float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ inline void from_f32(float x, __half &y) { y = __float2half_rn(x); }
-__device__ inline void from_f32(float x, __nv_bfloat16 &y) { y = __float2bfloat16_rn(x); }
+struct Meta {                            // one per CTA: the item it began and did not end
+    int32_t r, h, mt, last;              // r = -1: none; last = the CTA that ended it
+    int32_t rows, failed, pad0, pad1;
+};
 
-// Positions [lo, hi) that row (b, i) sees.
-__device__ inline void range_of(const Params &p, int b, int i, int64_t &lo, int64_t &hi) {
-    const int n = p.q_len ? min(max(p.q_len[b], 0), p.N) : p.N;
-    lo = hi = 0;
-    if (i >= n) return;
-    const int64_t pos = int64_t(max(p.kv_len[b], 0)) + i;
-    lo = p.window > 0 ? max(pos - p.window + 1, int64_t(0)) : 0;
-    hi = max(min(pos + 1, int64_t(p.max_pages) << p.page_shift), lo);
+struct Params {
+    CUtensorMap k_map, v_map;
+    const void *q;
+    int64_t qb, qn, qh;
+    const int32_t *table, *kv_len, *q_len;
+    int32_t B, N, Hq, Hkv, G, max_pages, pages, page_shift, window, ctas, part_rows, cache_rows;
+    float c;                             // |scale| * log2(e)
+    int32_t negate;
+    void *out;
+    float *lse;
+    Meta *meta;                          // [ctas]
+    float *parts;                        // [2 * ctas][D + 2][part_rows]: O, m, sum
+    uint64_t limit_ns;
+};
+
+// ---------------------------------------------------------------- the work ----
+// Request r's part of the work: tokens of the block, positions its rows see, tiles.
+struct Request {
+    int32_t n, kv;
+    int64_t lo, end;                     // some row sees positions [lo, end)
+    int32_t t0, nt, mts;                 // first tile, tiles, row tiles
+};
+
+__device__ inline Request request_of(const Params &p, int r) {
+    Request q;
+    q.n = p.q_len ? min(max(p.q_len[r], 0), p.N) : p.N;
+    q.kv = max(p.kv_len[r], 0);
+    q.end = min(int64_t(q.kv) + q.n, int64_t(p.max_pages) << p.page_shift);
+    q.lo = p.window > 0 ? max(int64_t(q.kv) - p.window + 1, int64_t(0)) : 0;
+    if (q.n == 0 || q.end <= q.lo) {
+        q.t0 = q.nt = 0;
+    } else {
+        q.t0 = int32_t(q.lo / kTile);
+        q.nt = int32_t((q.end + kTile - 1) / kTile) - q.t0;
+    }
+    q.mts = (q.n * p.G + kRows - 1) / kRows;
+    return q;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) part_kernel(Params p) {
-    constexpr int E = D / 32;
-    wait_for_prerequisite_grid();
-    allow_dependent_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t id = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t row = id / p.parts;
-    const int part = int(id - row * p.parts);
-    if (row >= int64_t(p.B) * p.N * p.Hq) return;
-    const int h = int(row % p.Hq);
-    const int i = int(row / p.Hq % p.N), b = int(row / p.Hq / p.N);
-    const int hk = h / (p.Hq / p.Hkv);
-    int64_t lo, hi;
-    range_of(p, b, i, lo, hi);
-    const int64_t span = hi - lo;
-    const int64_t j0 = lo + span * part / p.parts, j1 = lo + span * (part + 1) / p.parts;
-    const T *q = static_cast<const T *>(p.q) + b * p.qb + i * p.qn + h * p.qh;
-    float qr[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qr[e] = j1 > j0 ? to_f32(q[lane + 32 * e]) : 0.0f;
-        o[e] = 0.0f;
+__device__ inline int64_t units_of(const Params &p, const Request &q) { return int64_t(p.Hkv) * q.mts * q.nt; }
+
+// A CTA's walk over its range of units, item by item; every role takes the same steps.
+struct Walk {
+    int32_t r, h, mt;
+    Request q;
+    int32_t a, b;                        // this item's tiles [a, b) of [0, q.nt) are this CTA's
+    int64_t left;                        // units of the range not yet handed out, this item's excluded
+
+    __device__ void start(const Params &p, int32_t r0, int64_t off, int64_t count) {
+        r = r0;
+        left = count;
+        q = request_of(p, r);
+        a = b = 0;
+        if (count <= 0) return;
+        const int64_t item = off / q.nt;
+        h = int32_t(item / q.mts);
+        mt = int32_t(item % q.mts);
+        a = int32_t(off - item * q.nt);
+        take();
     }
-    float m = -INFINITY, s = 0.0f;
-    for (int64_t j = j0; j < j1; ++j) {
-        const int32_t page = p.table[int64_t(b) * p.max_pages + (j >> p.page_shift)];
-        const bool there = page >= 0 && page < p.pages;
-        const int64_t at = ((((int64_t(page) * p.Hkv + hk) << p.page_shift) + (j & ((1 << p.page_shift) - 1)))) * D;
-        float dot = 0.0f, v[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            v[e] = there ? to_f32(static_cast<const T *>(p.v_cache)[at + lane + 32 * e]) : 0.0f;
-            dot += there ? qr[e] * to_f32(static_cast<const T *>(p.k_cache)[at + lane + 32 * e]) : 0.0f;
+    __device__ void take() {
+        const int64_t can = q.nt - a;
+        const int32_t n = int32_t(left < can ? left : can);
+        b = a + n;
+        left -= n;
+    }
+    __device__ bool valid() const { return b > a; }
+    __device__ void next(const Params &p) {
+        if (left <= 0) {
+            a = b = 0;
+            return;
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-        dot *= p.scale;
-        const float m2 = fmaxf(m, dot);
-        const float f = m == m2 ? 1.0f : expf(m - m2), w = dot == m2 ? 1.0f : expf(dot - m2);
-        s = s * f + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * v[e];
-        m = m2;
+        a = 0;
+        if (++mt == q.mts) {
+            mt = 0;
+            if (++h == p.Hkv) {
+                h = 0;
+                do {                                     // left > 0: a later request has units
+                    if (++r >= p.B) {
+                        a = b = 0;
+                        return;
+                    }
+                    q = request_of(p, r);
+                } while (q.nt == 0);
+            }
+        }
+        take();
     }
-    float *ws = p.ws + (row * p.parts + part) * (D + 2);
-    if (lane == 0) {
-        ws[0] = m;
-        ws[1] = s;
+};
+
+// ------------------------------------------------------------------ tcgen05 ----
+__device__ inline void tc_alloc(uint32_t smem_out, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_out), "r"(cols) : "memory");
+}
+__device__ inline void tc_dealloc(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ inline void tc_relinquish() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ inline void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ inline void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ inline void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem], and the same with A in tensor memory.
+__device__ inline void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+__device__ inline void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+
+// 32 columns of this warp's 32 lanes, and the wait that makes them usable.
+__device__ inline void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ inline void tc_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ inline void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+        : "memory");
+}
+__device__ inline void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle: start, leading and stride byte
+// offsets in units of 16 bytes, version 1, layout 2.  K-major (Q, K): rows of 128
+// bytes, groups of 8 rows `stride` apart.  MN-major (V): 64 columns per 128-byte row,
+// groups of 8 rows `stride` apart, the next 64 columns `lead` away.
+__device__ inline uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return uint64_t((addr >> 4) & 0x3fff) | (uint64_t((lead >> 4) & 0x3fff) << 16) |
+           (uint64_t((stride >> 4) & 0x3fff) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Instruction descriptor of kind::f16: float32 accumulator, A K-major, B K-major or
+// (b_mn) MN-major, M = 128, N = n.
+template <typename T>
+__device__ constexpr uint32_t instr_desc(int n, bool b_mn);
+template <>
+__device__ constexpr uint32_t instr_desc<__half>(int n, bool b_mn) {
+    return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(n / 8) << 17) | (uint32_t(kRows / 16) << 24);
+}
+template <>
+__device__ constexpr uint32_t instr_desc<__nv_bfloat16>(int n, bool b_mn) {
+    return instr_desc<__half>(n, b_mn) | (1u << 7) | (1u << 10);
+}
+
+__device__ inline void tma_load(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ inline void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ inline float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two probabilities as one word of the type, the first in the low half.
+__device__ inline uint32_t pack2(float lo, float hi, __half) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ inline uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// ------------------------------------------------------------------- shared ----
+// Ahead of the tiles: barriers (8 bytes each) and a few words.
+struct Head {
+    uint64_t full[16], empty[16];        // slots
+    uint64_t s_full[2], p_ready[2], pv_done[2], q_ready, drain;
+    uint32_t tmem, failed;
+    int32_t start_r;
+    int64_t start_off, total;
+    int64_t warp_sum[kThreads / 32];
+};
+static_assert(sizeof(Head) <= kBarBytes, "Head fits ahead of the tiles");
+
+// Waits for phase `parity` of the barrier, at most limit_ns and only while no other
+// wait of the CTA has run out; false otherwise.
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
+    const uint64_t from = lkd::global_ns();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*failed) return false;
+        if (lkd::global_ns() - from > limit_ns) {
+            *failed = 1;
+            return false;
+        }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) ws[2 + lane + 32 * e] = o[e];
+}
+
+__device__ inline bool wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return slow_wait(bar, parity, failed, limit_ns);
+}
+
+// The same for a whole warp: every lane waits, and all go on or none does.
+__device__ inline bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, wait(bar, parity, failed, limit_ns));
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) join_kernel(Params p) {
-    constexpr int E = D / 32;
+__global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(const __grid_constant__ Params p) {
+    using S = Shape<D>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Head &hd = *reinterpret_cast<Head *>(smem);
+    const uint32_t q_smem = smem_addr(smem) + kBarBytes;
+    const uint32_t slots = q_smem + S::kQBytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    volatile uint32_t *failed = &hd.failed;
+    auto full = [&](int s) { return smem_addr(&hd.full[s]); };
+    auto empty = [&](int s) { return smem_addr(&hd.empty[s]); };
+
+    if (tid == 0) {
+        for (int s = 0; s < S::kSlots; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(smem_addr(&hd.s_full[k]), 1);
+            mbar_init(smem_addr(&hd.p_ready[k]), kRows);
+            mbar_init(smem_addr(&hd.pv_done[k]), 1);
+        }
+        mbar_init(smem_addr(&hd.q_ready), kRows);
+        mbar_init(smem_addr(&hd.drain), 1);
+        lkd::fence_barrier_init();
+        hd.failed = 0;
+    }
+    if (warp == kMmaWarp) {
+        tc_alloc(smem_addr(&hd.tmem), S::kCols);
+        tc_relinquish();
+    }
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    if (row >= int64_t(p.B) * p.N * p.Hq) return;
-    const float *ws = p.ws + row * p.parts * (D + 2);
-    float m = -INFINITY, s = 0.0f, o[E] = {};
-    for (int k = 0; k < p.parts; ++k, ws += D + 2) {
-        const float mk = ws[0];
-        if (ws[1] == 0.0f) continue;                     // an empty part
-        const float m2 = fmaxf(m, mk);
-        const float f = m == m2 ? 1.0f : expf(m - m2), w = mk == m2 ? 1.0f : expf(mk - m2);
-        s = s * f + w * ws[1];
+
+    // the range of this CTA: units [start, stop) of all requests' units end to end
+    {
+        int64_t own = 0;
+        for (int r = tid; r < p.B; r += kThreads) own += units_of(p, request_of(p, r));
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * ws[2 + lane + 32 * e];
-        m = m2;
+        for (int d = 16; d; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
+        if (lane == 0) hd.warp_sum[warp] = own;
     }
-    T *out = static_cast<T *>(p.out) + row * D;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = hd.tmem;
+    int64_t total = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) from_f32(s > 0.0f ? o[e] / s : 0.0f, out[lane + 32 * e]);
-    if (lane == 0 && p.lse) p.lse[row] = s > 0.0f ? m + logf(s) : -INFINITY;
+    for (int w = 0; w < kThreads / 32; ++w) total += hd.warp_sum[w];
+    const int64_t ctas = min(int64_t(p.ctas), total);    // with a range of their own
+    const int64_t start = cta < ctas ? total * cta / ctas : total, stop = cta < ctas ? total * (cta + 1) / ctas : total;
+    const int64_t count = stop - start;
+    if (count > 0) {
+        int64_t before = 0;                              // units of the requests ahead of this pass
+        for (int r0 = 0; r0 < p.B && before <= start; r0 += kThreads) {
+            const int r = r0 + tid;
+            const int64_t own = r < p.B ? units_of(p, request_of(p, r)) : 0;
+            int64_t incl = own;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += y;
+            }
+            __syncthreads();                             // warp_sum's last readers are done
+            if (lane == 31) hd.warp_sum[warp] = incl;
+            __syncthreads();
+            int64_t ahead = before;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) ahead += hd.warp_sum[w];
+                before += hd.warp_sum[w];
+            }
+            if (ahead + incl - own <= start && start < ahead + incl) {
+                hd.start_r = r;
+                hd.start_off = start - (ahead + incl - own);
+            }
+        }
+    }
+    __syncthreads();
+
+    Walk wk;
+    if (count > 0) wk.start(p, hd.start_r, hd.start_off, count);
+
+    if (count > 0 && warp == kLoadWarp) {
+        // ---- loads: K and V of tile after tile, slot after slot ----
+        const int box_rows = min(kTile, 1 << p.page_shift);
+        const int per_tile = kTile / box_rows;           // pages of a tile (1 when a page holds whole tiles)
+        const int boxes = per_tile * (D / 64);           // at most 8 * 4
+        const int my_page = lane % per_tile, my_col = lane / per_tile;
+        uint32_t n = 0;                                  // slots filled so far
+        bool ok = true;
+        for (; ok && wk.valid(); wk.next(p)) {
+            const int32_t *table = p.table + int64_t(wk.r) * p.max_pages;
+            auto entry = [&](int64_t at) { return at < p.max_pages ? table[at] : -1; };
+            // page ids, 32 at a time, and the next 32 ahead of their use
+            const int64_t x_first = int64_t(wk.q.t0 + wk.a) * kTile;
+            int64_t base = x_first >> p.page_shift;
+            int32_t cur = entry(base + lane), nxt = entry(base + 32 + lane);
+            for (int t = wk.a; ok && t < wk.b; ++t) {
+                const int64_t x0 = int64_t(wk.q.t0 + t) * kTile;
+                int64_t at = x0 >> p.page_shift;
+                if (at - base >= 32) {                   // a tile's pages never straddle a window: 32 % per_tile == 0
+                    base += 32;
+                    cur = nxt;
+                    nxt = entry(base + 32 + lane);
+                }
+                const int32_t page = __shfl_sync(0xffffffffu, cur, int(at - base) + my_page);
+                const int64_t x = x0 + my_page * box_rows;
+                // a row past the map's end reads as zeros: absent pages, and pages past the end
+                int32_t y = p.cache_rows;
+                if (page >= 0 && page < p.pages && x < wk.q.end)
+                    y = ((page * p.Hkv + wk.h) << p.page_shift) + int32_t(x & ((1 << p.page_shift) - 1));
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int s = n % S::kSlots;
+                    if (!warp_wait(empty(s), ((n / S::kSlots) & 1) ^ 1, failed, p.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_expect_tx(full(s), S::kSlotBytes);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load(slots + s * S::kSlotBytes + my_col * (kTile * 128) + my_page * box_rows * 128,
+                                 kv ? &p.v_map : &p.k_map, my_col * 64, y, full(s));
+                }
+            }
+        }
+        {                                                // no copy outlives the CTA, whoever gave up
+            const uint32_t in_flight = n < uint32_t(S::kSlots) ? n : uint32_t(S::kSlots);
+            for (uint32_t k = n - in_flight; k < n; ++k) {
+                const uint64_t until = lkd::global_ns() + 1000000000ull;
+                while (!mbar_try_wait(full(k % S::kSlots), (k / S::kSlots) & 1) && lkd::global_ns() < until) {
+                }
+            }
+        }
+    } else if (count > 0 && warp == kMmaWarp) {
+        // ---- products, by one thread ----
+        if (lane == 0) {
+            constexpr uint32_t kQk = instr_desc<T>(kTile, false), kPv = instr_desc<T>(D, true);
+            uint32_t it = 0, item = 0;                   // tiles and items so far
+            bool ok = true;
+            auto pv = [&](uint32_t k, bool first) {      // tile k's P V into O
+                const uint32_t n = 2 * k + 1;
+                const int s = n % S::kSlots;
+                ok = wait(smem_addr(&hd.p_ready[k & 1]), (k >> 1) & 1, failed, p.limit_ns) &&
+                     wait(full(s), (n / S::kSlots) & 1, failed, p.limit_ns);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t v = slots + s * S::kSlotBytes;
+#pragma unroll
+                for (int j = 0; j < kTile / 16; ++j)
+                    tc_mma_ts(tmem + S::kO, tmem + (k & 1) * kTile + j * 8, operand_desc(v + j * 2048, kTile * 128, 1024),
+                              kPv, !(first && j == 0));
+                tc_commit(empty(s));
+                tc_commit(smem_addr(&hd.pv_done[k & 1]));
+            };
+            for (; ok && wk.valid(); wk.next(p), ++item) {
+                ok = wait(smem_addr(&hd.q_ready), item & 1, failed, p.limit_ns);
+                for (int t = wk.a; ok && t < wk.b; ++t, ++it) {
+                    const uint32_t n = 2 * it;
+                    const int s = n % S::kSlots;
+                    // K is there, and P of two tiles ago, which S overwrites, has been used
+                    ok = wait(full(s), (n / S::kSlots) & 1, failed, p.limit_ns) &&
+                         (it < 2 || wait(smem_addr(&hd.pv_done[it & 1]), ((it >> 1) - 1) & 1, failed, p.limit_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t k = slots + s * S::kSlotBytes;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        tc_mma_ss(tmem + (it & 1) * kTile,
+                                  operand_desc(q_smem + (j / 4) * (kRows * 128) + (j % 4) * 32, 16, 1024),
+                                  operand_desc(k + (j / 4) * (kTile * 128) + (j % 4) * 32, 16, 1024), kQk, j > 0);
+                    tc_commit(empty(s));
+                    tc_commit(smem_addr(&hd.s_full[it & 1]));
+                    if (t > wk.a) pv(it - 1, t - 1 == wk.a);
+                }
+                if (ok) pv(it - 1, wk.b - 1 == wk.a);
+            }
+            {                                            // nor does a product
+                tc_commit(smem_addr(&hd.drain));
+                const uint64_t until = lkd::global_ns() + 1000000000ull;
+                while (!mbar_try_wait(smem_addr(&hd.drain), 0) && lkd::global_ns() < until) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < kSoftWarps) {
+        // ---- softmax: a thread per row ----
+        const uint32_t lanes = uint32_t(warp * 32) << 16;
+        const int row = warp * 32 + lane;
+        uint32_t it = 0;
+        Meta meta{-1, 0, 0, 0, 0, 0, 0, 0};
+        bool ok = true;
+        // rows of the block past q_len, and those of requests that see nothing
+        for (int r = cta; r < p.B; r += p.ctas) {
+            const Request q = request_of(p, r);
+            const int64_t i0 = (int64_t(r) * p.N + (q.nt ? q.n : 0)) * p.Hq, i1 = int64_t(r + 1) * p.N * p.Hq;
+            for (int64_t x = i0 * (D / 8) + row; x < i1 * (D / 8); x += kRows)
+                reinterpret_cast<uint4 *>(p.out)[x] = make_uint4(0, 0, 0, 0);
+            if (p.lse)
+                for (int64_t x = i0 + row; x < i1; x += kRows) p.lse[x] = -INFINITY;
+        }
+        for (; count > 0 && ok && wk.valid(); wk.next(p)) {
+            const Request &q = wk.q;
+            const int rows = min(kRows, q.n * p.G - wk.mt * kRows);
+            const int rr = wk.mt * kRows + row;          // row of the request: token, then head of the group
+            const bool live = row < rows;
+            const int i = live ? rr / p.G : 0;
+            const int head = wk.h * p.G + (live ? rr - i * p.G : 0);
+            // Q, 16 bytes at a time, where the products' swizzle wants it; idle rows are zeros
+            {
+                const T *src = static_cast<const T *>(p.q) + wk.r * p.qb + wk.h * p.G * p.qh;
+                for (int x = row; x < kRows * (D / 8); x += kRows) {
+                    const int y = x / (D / 8), ch = x % (D / 8);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (y < rows) {
+                        const int ry = wk.mt * kRows + y, iy = ry / p.G;
+                        v = *reinterpret_cast<const uint4 *>(src + iy * p.qn + (ry - iy * p.G) * p.qh + ch * 8);
+                        if (p.negate) {
+                            v.x ^= 0x80008000u;
+                            v.y ^= 0x80008000u;
+                            v.z ^= 0x80008000u;
+                            v.w ^= 0x80008000u;
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(smem + kBarBytes + (ch >> 3) * (kRows * 128) + y * 128 +
+                                               (((ch & 7) ^ (y & 7)) << 4)) = v;
+                }
+                lkd::fence_proxy_async_smem();
+                mbar_arrive(smem_addr(&hd.q_ready));
+            }
+            // positions this row sees: [see0, see1)
+            const int64_t pos = int64_t(q.kv) + i;
+            const int64_t see1 = min(pos + 1, q.end);
+            const int64_t see0 = p.window > 0 ? max(pos - p.window + 1, int64_t(0)) : 0;
+            float m = -INFINITY, sum = 0.0f;             // m: the raw product the sums are relative to
+            const bool warp_live = warp * 32 < rows;
+            for (int t = wk.a; t < wk.b; ++t, ++it) {
+                const int64_t x0 = int64_t(q.t0 + t) * kTile;
+                if (!warp_wait(smem_addr(&hd.s_full[it & 1]), (it >> 1) & 1, failed, p.limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (x0 < q.lo || x0 + kTile > q.end) {
+                    // rows of V that no row of the block sees may hold anything: zeros
+                    const uint32_t n = 2 * it + 1;
+                    const int s = n % S::kSlots;
+                    if (!warp_wait(full(s), (n / S::kSlots) & 1, failed, p.limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char *v = smem + kBarBytes + S::kQBytes + s * S::kSlotBytes;
+                    for (int x = row; x < kTile * (D / 8); x += kRows) {
+                        const int y = (x >> 3) & (kTile - 1);
+                        if (x0 + y < q.lo || x0 + y >= q.end)
+                            *reinterpret_cast<uint4 *>(v + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    lkd::fence_proxy_async_smem();
+                }
+                if (warp_live) {
+                    const uint32_t at = tmem + lanes + (it & 1) * kTile;
+                    uint32_t r0[32], r1[32];
+                    tc_ld32(at, r0);
+                    tc_ld32(at + 32, r1);
+                    tc_wait_ld(r0);
+                    tc_wait_ld(r1);
+                    // tiles that some row of the request sees less than all of
+                    const bool masked = x0 + kTile > min(int64_t(q.kv) + 1, q.end) ||
+                                        (p.window > 0 && x0 < int64_t(q.kv) + q.n - p.window);
+                    if (masked) {
+                        const int c0 = int(min(max(see0 - x0, int64_t(0)), int64_t(kTile)));
+                        const int c1 = int(min(max(see1 - x0, int64_t(0)), int64_t(kTile)));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if (j < c0 || j >= c1) r0[j] = 0xff800000u;
+                            if (j + 32 < c0 || j + 32 >= c1) r1[j] = 0xff800000u;
+                        }
+                    }
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fmaxf(__uint_as_float(r0[j]), __uint_as_float(r1[j])));
+                    const bool fresh = t == wk.a;
+                    bool lift = mx > m && (fresh || m == -INFINITY || (mx - m) * p.c > kLazy);
+                    if (fresh) {
+                        m = mx;
+                    } else if (__any_sync(0xffffffffu, lift)) {
+                        // bring O and the sum to the new m; P V of the tile before has to be in O
+                        if (!warp_wait(smem_addr(&hd.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, failed, p.limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const float f = !lift ? 1.0f : (m == -INFINITY ? 0.0f : exp2_approx((m - mx) * p.c));
+                        if (lift) m = mx;
+                        sum *= f;
+#pragma unroll
+                        for (int j = 0; j < D; j += 32) {
+                            uint32_t o[32];
+                            tc_ld32(tmem + lanes + S::kO + j, o);
+                            tc_wait_ld(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                o[k] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(o[k]) * f);
+                            tc_st32(tmem + lanes + S::kO + j, o);
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.0f : m * p.c;
+                    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float x0f = __uint_as_float(r0[j]), x1f = __uint_as_float(r0[j + 1]);
+                        const float y0f = __uint_as_float(r1[j]), y1f = __uint_as_float(r1[j + 1]);
+                        float a0 = exp2_approx(fmaf(x0f, p.c, -mc)), a1 = exp2_approx(fmaf(x1f, p.c, -mc));
+                        float b0 = exp2_approx(fmaf(y0f, p.c, -mc)), b1 = exp2_approx(fmaf(y1f, p.c, -mc));
+                        if (masked) {                    // also where c is 0
+                            a0 = r0[j] == 0xff800000u ? 0.0f : a0;
+                            a1 = r0[j + 1] == 0xff800000u ? 0.0f : a1;
+                            b0 = r1[j] == 0xff800000u ? 0.0f : b0;
+                            b1 = r1[j + 1] == 0xff800000u ? 0.0f : b1;
+                        }
+                        s0 += a0;
+                        s1 += a1;
+                        s2 += b0;
+                        s3 += b1;
+                        w[j / 2] = pack2(a0, a1, T());
+                        w[16 + j / 2] = pack2(b0, b1, T());
+                    }
+                    sum += (s0 + s1) + (s2 + s3);
+                    tc_st32(at, w);
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(smem_addr(&hd.p_ready[it & 1]));
+            }
+            if (!ok) break;
+            if (!warp_wait(smem_addr(&hd.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, failed, p.limit_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // the item's end: its rows, or this CTA's part of them
+            const bool whole = wk.a == 0 && wk.b == q.nt;
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const int64_t o_row = (int64_t(wk.r) * p.N + i) * p.Hq + head;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + o_row * D);
+                if (warp_live) {
+#pragma unroll
+                    for (int j = 0; j < D; j += 32) {
+                        uint32_t o[32];
+                        tc_ld32(tmem + lanes + S::kO + j, o);
+                        tc_wait_ld(o);
+                        if (live) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float lo = __uint_as_float(o[k + 2 * e]) * inv;
+                                    const float hi = __uint_as_float(o[k + 2 * e + 1]) * inv;
+                                    w[e] = sum == 0.0f ? 0u : pack2(lo, hi, T());   // a row that sees nothing
+                                }
+                                dst[(j + k) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                    }
+                    if (live && p.lse)
+                        p.lse[o_row] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (m * p.c + log2f(sum));
+                }
+            } else {
+                // slot 2c + 1: the item began here; 2c: it began in an earlier range
+                const int slot = 2 * cta + (wk.a == 0 ? 1 : 0);
+                float *ws = p.parts + int64_t(slot) * (D + 2) * p.part_rows;
+                if (warp_live) {
+#pragma unroll
+                    for (int j = 0; j < D; j += 32) {
+                        uint32_t o[32];
+                        tc_ld32(tmem + lanes + S::kO + j, o);
+                        tc_wait_ld(o);
+                        if (live) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) ws[(j + k) * p.part_rows + row] = __uint_as_float(o[k]);
+                        }
+                    }
+                    if (live) {
+                        ws[D * p.part_rows + row] = m;
+                        ws[(D + 1) * p.part_rows + row] = sum;
+                    }
+                }
+                if (wk.a == 0) {
+                    // the CTA that has the item's last unit: the largest c whose range starts at or before it
+                    const int64_t end = stop + (q.nt - wk.b);
+                    int64_t last = (end - 1) * ctas / total;
+                    while (last + 1 < ctas && total * (last + 1) / ctas <= end - 1) ++last;
+                    while (total * last / ctas > end - 1) --last;
+                    meta = Meta{wk.r, wk.h, wk.mt, int32_t(last), rows, 0, 0, 0};
+                }
+            }
+            tc_fence_before();                           // O is read before the next item's products (p_ready)
+        }
+        if (row == 0) {
+            meta.failed = ok ? 0 : 1;
+            p.meta[cta] = meta;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tc_dealloc(tmem, S::kCols);
+    // a wait that ran out in a role that does not write the record
+    if (tid == 0 && hd.failed) p.meta[cta].failed = 1;
 }
 
-int parts_for(int64_t rows) {
-    const int64_t want = 152 * 64 / (rows > 0 ? rows : 1) + 1;
-    return int(want > kMaxParts ? kMaxParts : want);
+// Joins the parts of the item that CTA blockIdx.x of attention_kernel began and did
+// not end: kJoinRows of its rows.  First every part's weight 2^(c (m_k - M)) / sum
+// for each row, all loads at once; then a thread per (column, row) adds the parts,
+// their loads independent of each other.  (A running maximum over the parts, one
+// load waiting for the last, took 38 us for 52 parts.)  A wait that ran out anywhere
+// makes the whole call's rows NaN.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+    __shared__ float weight[kJoinRows][kMaxCtas];
+    __shared__ float s_inv[kJoinRows];
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+    const Meta meta = p.meta[c];
+    int bad = 0;
+    for (int k = tid; k < p.ctas; k += kJoinThreads) bad |= p.meta[k].failed;
+    if (__syncthreads_or(bad)) {
+        const int64_t rows = int64_t(p.B) * p.N * p.Hq;
+        const int64_t first = (int64_t(blockIdx.y) * gridDim.x + c) * kJoinThreads + tid;
+        const int64_t step = int64_t(gridDim.x) * gridDim.y * kJoinThreads;
+        for (int64_t x = first; x < rows * D; x += step) static_cast<T *>(p.out)[x] = T(NAN);
+        if (p.lse)
+            for (int64_t x = first; x < rows; x += step) p.lse[x] = NAN;
+        return;
+    }
+    const int row0 = blockIdx.y * kJoinRows;
+    if (meta.r < 0 || row0 >= meta.rows) return;
+    const int64_t size = int64_t(D + 2) * p.part_rows;   // of a part
+    const int count = meta.last - c + 1;
+    const float *own = p.parts + int64_t(2 * c + 1) * size, *more = p.parts + int64_t(2 * c + 2) * size;   // then every second
+    auto part = [&](int k) { return k ? more + int64_t(2 * (k - 1)) * size : own; };
+    auto place = [&](int row) {                          // the row's place in out / D and in lse
+        const int rr = meta.mt * kRows + row, i = rr / p.G;
+        return (int64_t(meta.r) * p.N + i) * p.Hq + meta.h * p.G + (rr - i * p.G);
+    };
+    {
+        const int row = row0 + (tid >> 5);               // a warp per row
+        if (row < meta.rows) {
+            float big = -INFINITY, sum = 0.0f;
+            for (int k = lane; k < count; k += 32) {
+                const float mk = part(k)[D * p.part_rows + row], sk = part(k)[(D + 1) * p.part_rows + row];
+                weight[tid >> 5][k] = sk == 0.0f ? -INFINITY : mk;       // a part the row sees nothing of
+                if (sk != 0.0f) big = fmaxf(big, mk);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+            for (int k = lane; k < count; k += 32) {
+                const float mk = weight[tid >> 5][k];
+                const float w = mk == -INFINITY ? 0.0f : exp2f((mk - big) * p.c);
+                weight[tid >> 5][k] = w;
+                if (w != 0.0f) sum += w * part(k)[(D + 1) * p.part_rows + row];
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0) {
+                s_inv[tid >> 5] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                if (p.lse)
+                    p.lse[place(row)] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(sum));
+            }
+        }
+    }
+    __syncthreads();
+    for (int x = tid; x < kJoinRows * D; x += kJoinThreads) {
+        const int y = x % kJoinRows, row = row0 + y, col = x / kJoinRows;
+        if (row >= meta.rows) continue;
+        float o = 0.0f;
+#pragma unroll 8
+        for (int k = 0; k < count; ++k) {
+            const float w = weight[y][k], v = part(k)[col * p.part_rows + row];
+            o += w == 0.0f ? 0.0f : w * v;
+        }
+        static_cast<T *>(p.out)[place(row) * D + col] = T(o * s_inv[y]);
+    }
+}
+
+// -------------------------------------------------------------------- host ----
+int cuda_fail(cudaError_t e, const char *what) { return lookup_record_cuda_error(e, what); }
+
+// CTAs of a call: as many as run at once on the device.
+int ctas_for(int D, int sms) { return sms * (D == 256 ? 1 : 2); }
+
+int part_rows_for(int64_t N, int64_t G) { return int(N * G < kRows ? N * G : kRows); }
+
+size_t workspace_for(int32_t N, int32_t G, int32_t D) {
+    const size_t ctas = size_t(ctas_for(D, kMaxSms));
+    return ctas * sizeof(Meta) + ctas * 2 * size_t(D + 2) * size_t(part_rows_for(N, G)) * sizeof(float);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+int encode_fn(EncodeTiled *out) {
+    static std::atomic<EncodeTiled> known{nullptr};
+    EncodeTiled fn = known.load(std::memory_order_acquire);
+    if (!fn) {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult st;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &st);
+        if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled");
+        if (st != cudaDriverEntryPointSuccess || !f) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled");
+        fn = reinterpret_cast<EncodeTiled>(f);
+        known.store(fn, std::memory_order_release);
+    }
+    *out = fn;
+    return LOOKUP_DRAFT_OK;
+}
+
+// The cache as rows of D elements; a box is 64 columns by one page's rows of a tile.
+int cache_map(EncodeTiled fn, CUtensorMap *map, const void *base, int32_t type, int D, int64_t rows, int box_rows) {
+    const cuuint64_t dims[2] = {cuuint64_t(D), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(D) * 2};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, elem[2] = {1, 1};
+    const CUresult e =
+        fn(map, type == LOOKUP_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+           const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return e == CUDA_SUCCESS ? LOOKUP_DRAFT_OK : cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
 }
 
 template <typename T, int D>
-int launch(const Params &p, cudaStream_t stream) {
-    const int64_t rows = int64_t(p.B) * p.N * p.Hq;
-    const int rc = launch_pdl(part_kernel<T, D>, unsigned((rows * p.parts + kWarps - 1) / kWarps),
-                              unsigned(kWarps * 32), stream, p);
-    if (rc != LOOKUP_DRAFT_OK) return rc;
-    return launch_pdl(join_kernel<T, D>, unsigned((rows + kWarps - 1) / kWarps), unsigned(kWarps * 32), stream, p);
+int launch(Params &p, cudaStream_t stream) {
+    using S = Shape<D>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "shared-memory opt-in");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t r = cudaLaunchKernelEx(&cfg, attention_kernel<T, D>, p);
+    if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
+    lookup_note_launch();
+    cfg.gridDim = dim3(p.ctas, (p.part_rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    r = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p);
+    if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
+    lookup_note_launch();
+    return LOOKUP_DRAFT_OK;
 }
 
 template <typename T>
-int launch_d(const Params &p, int D, cudaStream_t stream) {
+int launch_d(Params &p, int D, cudaStream_t stream) {
     return D == 64 ? launch<T, 64>(p, stream) : D == 128 ? launch<T, 128>(p, stream) : launch<T, 256>(p, stream);
 }
 
@@ -157,8 +892,7 @@ extern "C" {
 
 size_t lookup_paged_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D) {
     if (B < 0 || N < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
-    const int64_t rows = int64_t(B) * N * Hq;
-    return size_t(rows) * size_t(parts_for(rows)) * size_t(D + 2) * sizeof(float) + 16;
+    return workspace_for(N, Hq / Hkv, D);
 }
 
 int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *k_cache, const void *v_cache,
@@ -171,10 +905,12 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
         pages < 1 || page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) || window < 0 ||
         !(std::fabs(scale) < INFINITY) || (type != LOOKUP_TYPE_F16 && type != LOOKUP_TYPE_BF16))
         return LOOKUP_DRAFT_EINVAL;
-    if (int64_t(pages) * Hkv * page_size > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
+    const int64_t cache_rows = int64_t(pages) * Hkv * page_size;
+    if (cache_rows > INT32_MAX - 2 * kTile || int64_t(max_pages) * page_size > INT32_MAX - 2 * kTile)
+        return LOOKUP_DRAFT_EINVAL;
     if (B == 0 || N == 0) return LOOKUP_DRAFT_OK;
     const int64_t rows = int64_t(B) * N * Hq;
-    if (rows > (int64_t(1) << 30)) return LOOKUP_DRAFT_EINVAL;
+    if (int64_t(N) * Hq > (1 << 30) || rows > (int64_t(1) << 30)) return LOOKUP_DRAFT_EINVAL;
     if (!q || !q_strides || !k_cache || !v_cache || !block_table || !kv_len || !out || !workspace)
         return LOOKUP_DRAFT_EINVAL;
     for (const void *x : {q, k_cache, v_cache, static_cast<const void *>(workspace), static_cast<const void *>(out)})
@@ -183,14 +919,30 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
         if (q_strides[k] & 7) return LOOKUP_DRAFT_EINVAL;
     if (misaligned(block_table, 4) || misaligned(kv_len, 4) || misaligned(q_len, 4) || misaligned(lse, 4))
         return LOOKUP_DRAFT_EINVAL;
-    if (workspace_bytes < lookup_paged_attention_workspace_bytes(B, N, Hq, Hkv, D)) return LOOKUP_DRAFT_EINVAL;
+    const int G = Hq / Hkv;
+    if (workspace_bytes < workspace_for(N, G, D)) return LOOKUP_DRAFT_EINVAL;
+    int sms = 0;
+    int rc = lkd::sm_count(&sms);
+    if (rc != LOOKUP_DRAFT_OK) return rc;
     Params p{};
+    EncodeTiled fn = nullptr;
+    rc = encode_fn(&fn);
+    const int box_rows = page_size < kTile ? page_size : kTile;
+    if (rc == LOOKUP_DRAFT_OK) rc = cache_map(fn, &p.k_map, k_cache, type, D, cache_rows, box_rows);
+    if (rc == LOOKUP_DRAFT_OK) rc = cache_map(fn, &p.v_map, v_cache, type, D, cache_rows, box_rows);
+    if (rc != LOOKUP_DRAFT_OK) return rc;
     p.q = q, p.qb = q_strides[0], p.qn = q_strides[1], p.qh = q_strides[2];
-    p.k_cache = k_cache, p.v_cache = v_cache, p.table = block_table, p.kv_len = kv_len, p.q_len = q_len;
-    p.B = B, p.N = N, p.Hq = Hq, p.Hkv = Hkv, p.max_pages = max_pages, p.pages = pages;
+    p.table = block_table, p.kv_len = kv_len, p.q_len = q_len;
+    p.B = B, p.N = N, p.Hq = Hq, p.Hkv = Hkv, p.G = G, p.max_pages = max_pages, p.pages = pages;
     while ((1 << p.page_shift) < page_size) ++p.page_shift;
-    p.window = window, p.parts = parts_for(rows), p.scale = scale, p.out = out, p.lse = lse;
-    p.ws = static_cast<float *>(workspace);
+    p.window = window, p.ctas = ctas_for(D, sms < kMaxSms ? sms : kMaxSms), p.part_rows = part_rows_for(N, G);
+    p.cache_rows = int32_t(cache_rows);
+    p.c = std::fabs(scale) * 1.4426950408889634f;
+    p.negate = scale < 0.0f;
+    p.out = out, p.lse = lse;
+    p.meta = static_cast<Meta *>(workspace);
+    p.parts = reinterpret_cast<float *>(p.meta + p.ctas);
+    p.limit_ns = lookup_wait_limit_ns();
     return type == LOOKUP_TYPE_F16 ? launch_d<__half>(p, D, stream) : launch_d<__nv_bfloat16>(p, D, stream);
 }
 

@@ -265,6 +265,21 @@ def test_attention_infinite_value_reaches_its_rows():
     assert bool(out[..., :9].isfinite().all()) and bool(out[..., 10:].isfinite().all())
 
 
+def test_attention_waits_that_run_out_give_nan():
+    """A wait limit of a nanosecond: the call ends, every row says so, and the next call is
+    right again."""
+    case = attention_case([300, 31, 5000], [4, 3, 4], 4, 4, 2, 128, 16, BF16, 22)
+    q, kc, vc, table, kv, ql = (x.cuda() for x in case)
+    pkg.set_wait_limit_ns(1)
+    try:
+        out, lse = pkg.lookup_paged_attention(q, kc, vc, table, kv, q_len=ql)
+        torch.cuda.synchronize()
+    finally:
+        pkg.set_wait_limit_ns(0)
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
+    check_attention(*case)
+
+
 # ------------------------------------------------------------------ verify ----
 def verify_case(B, P, V, dt, mode, seed, pad=0, temps=None):
     g = gen(seed)
