@@ -55,6 +55,7 @@ constexpr int kJoinRows = 8;             // rows a CTA of join_kernel finishes
 constexpr int kJoinThreads = 32 * kJoinRows;
 constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
 constexpr int kMaxCtas = 2 * kMaxSms;
+constexpr int kItemUnits = 3;            // what an item's begin and end cost, in tiles
 constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
 constexpr int kBarBytes = 1024;          // barriers and small state ahead of the tiles
 
@@ -86,7 +87,7 @@ struct Params {
     void *out;
     float *lse;
     Meta *meta;                          // [ctas]
-    float *parts;                        // [2 * ctas][D + 2][part_rows]: O, m, sum
+    float *parts;                        // [2 * ctas]: O [part_rows][D], m [part_rows], sum [part_rows]
     uint64_t limit_ns;
 };
 
@@ -114,13 +115,19 @@ __device__ inline Request request_of(const Params &p, int r) {
     return q;
 }
 
-__device__ inline int64_t units_of(const Params &p, const Request &q) { return int64_t(p.Hkv) * q.mts * q.nt; }
+// Units: an item's tiles, after kItemUnits for its begin and end (its Q, its result), so
+// that a CTA with many short items gets fewer tiles.
+__device__ inline int32_t item_units(const Request &q) { return q.nt ? q.nt + kItemUnits : 0; }
+__device__ inline int64_t units_of(const Params &p, const Request &q) {
+    return int64_t(p.Hkv) * q.mts * item_units(q);
+}
 
 // A CTA's walk over its range of units, item by item; every role takes the same steps.
 struct Walk {
     int32_t r, h, mt;
     Request q;
-    int32_t a, b;                        // this item's tiles [a, b) of [0, q.nt) are this CTA's
+    int32_t u;                           // this item's first unit in the range
+    int32_t a, b;                        // its tiles [a, b) of [0, q.nt) are this CTA's; b = 0: none
     int64_t left;                        // units of the range not yet handed out, this item's excluded
 
     __device__ void start(const Params &p, int32_t r0, int64_t off, int64_t count) {
@@ -129,39 +136,38 @@ struct Walk {
         q = request_of(p, r);
         a = b = 0;
         if (count <= 0) return;
-        const int64_t item = off / q.nt;
+        const int64_t item = off / item_units(q);
         h = int32_t(item / q.mts);
         mt = int32_t(item % q.mts);
-        a = int32_t(off - item * q.nt);
+        u = int32_t(off - item * item_units(q));
         take();
+        if (b == 0) next(p);
     }
     __device__ void take() {
-        const int64_t can = q.nt - a;
+        const int64_t can = item_units(q) - u;
         const int32_t n = int32_t(left < can ? left : can);
-        b = a + n;
+        a = max(u - kItemUnits, 0);
+        b = max(u + n - kItemUnits, 0);
         left -= n;
     }
-    __device__ bool valid() const { return b > a; }
+    __device__ bool valid() const { return b > 0; }
     __device__ void next(const Params &p) {
-        if (left <= 0) {
+        do {
             a = b = 0;
-            return;
-        }
-        a = 0;
-        if (++mt == q.mts) {
-            mt = 0;
-            if (++h == p.Hkv) {
-                h = 0;
-                do {                                     // left > 0: a later request has units
-                    if (++r >= p.B) {
-                        a = b = 0;
-                        return;
-                    }
-                    q = request_of(p, r);
-                } while (q.nt == 0);
+            if (left <= 0) return;
+            u = 0;
+            if (++mt == q.mts) {
+                mt = 0;
+                if (++h == p.Hkv) {
+                    h = 0;
+                    do {                                 // left > 0: a later request has units
+                        if (++r >= p.B) return;
+                        q = request_of(p, r);
+                    } while (q.nt == 0);
+                }
             }
-        }
-        take();
+            take();
+        } while (b == 0);                                // the range ends before the item's first tile
     }
 };
 
@@ -525,24 +531,24 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             const bool live = row < rows;
             const int i = live ? rr / p.G : 0;
             const int head = wk.h * p.G + (live ? rr - i * p.G : 0);
-            // Q, 16 bytes at a time, where the products' swizzle wants it; idle rows are zeros
+            // Q, 16 bytes at a time, where the products' swizzle wants it (idle rows keep what
+            // was there: a row of S depends on its own row of Q only)
             {
-                const T *src = static_cast<const T *>(p.q) + wk.r * p.qb + wk.h * p.G * p.qh;
-                for (int x = row; x < kRows * (D / 8); x += kRows) {
-                    const int y = x / (D / 8), ch = x % (D / 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (y < rows) {
-                        const int ry = wk.mt * kRows + y, iy = ry / p.G;
-                        v = *reinterpret_cast<const uint4 *>(src + iy * p.qn + (ry - iy * p.G) * p.qh + ch * 8);
-                        if (p.negate) {
-                            v.x ^= 0x80008000u;
-                            v.y ^= 0x80008000u;
-                            v.z ^= 0x80008000u;
-                            v.w ^= 0x80008000u;
-                        }
+                constexpr int kCh = D / 8, kStep = kRows / kCh;          // chunks of a row, rows of a pass
+                const int ch = row % kCh;
+                const T *src = static_cast<const T *>(p.q) + wk.r * p.qb + wk.h * p.G * p.qh + ch * 8;
+                unsigned char *dst = smem + kBarBytes + (ch >> 3) * (kRows * 128);
+#pragma unroll 4
+                for (int y = row / kCh; y < rows; y += kStep) {
+                    const uint32_t ry = wk.mt * kRows + y, iy = ry / uint32_t(p.G);
+                    uint4 v = *reinterpret_cast<const uint4 *>(src + iy * p.qn + (ry - iy * p.G) * p.qh);
+                    if (p.negate) {
+                        v.x ^= 0x80008000u;
+                        v.y ^= 0x80008000u;
+                        v.z ^= 0x80008000u;
+                        v.w ^= 0x80008000u;
                     }
-                    *reinterpret_cast<uint4 *>(smem + kBarBytes + (ch >> 3) * (kRows * 128) + y * 128 +
-                                               (((ch & 7) ^ (y & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4 *>(dst + y * 128 + (((ch & 7) ^ (y & 7)) << 4)) = v;
                 }
                 lkd::fence_proxy_async_smem();
                 mbar_arrive(smem_addr(&hd.q_ready));
@@ -699,7 +705,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         tc_wait_ld(o);
                         if (live) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) ws[(j + k) * p.part_rows + row] = __uint_as_float(o[k]);
+                            for (int k = 0; k < 32; k += 4)
+                                *reinterpret_cast<uint4 *>(ws + row * D + j + k) =
+                                    make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                         }
                     }
                     if (live) {
@@ -709,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                 }
                 if (wk.a == 0) {
                     // the CTA that has the item's last unit: the largest c whose range starts at or before it
-                    const int64_t end = stop + (q.nt - wk.b);
+                    const int64_t end = stop + (q.nt - wk.b);            // of the item's units
                     int64_t last = (end - 1) * ctas / total;
                     while (last + 1 < ctas && total * (last + 1) / ctas <= end - 1) ++last;
                     while (total * last / ctas > end - 1) --last;
@@ -732,15 +740,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
 }
 
 // Joins the parts of the item that CTA blockIdx.x of attention_kernel began and did
-// not end: kJoinRows of its rows.  First every part's weight 2^(c (m_k - M)) / sum
-// for each row, all loads at once; then a thread per (column, row) adds the parts,
-// their loads independent of each other.  (A running maximum over the parts, one
-// load waiting for the last, took 38 us for 52 parts.)  A wait that ran out anywhere
-// makes the whole call's rows NaN.
+// not end, a warp per row: the weights 2^(c (m_k - M)) of the row's parts, a lane per
+// part, then the sum of the parts, a lane per D / 32 columns, its loads independent
+// of each other.  A wait that ran out anywhere makes the whole call's rows NaN.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
-    __shared__ float weight[kJoinRows][kMaxCtas];
-    __shared__ float s_inv[kJoinRows];
+    constexpr int E = D / 32;                            // columns of a lane
+    __shared__ float weights[kJoinRows][kMaxCtas];
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
@@ -756,54 +762,50 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             for (int64_t x = first; x < rows; x += step) p.lse[x] = NAN;
         return;
     }
-    const int row0 = blockIdx.y * kJoinRows;
-    if (meta.r < 0 || row0 >= meta.rows) return;
+    const int row = blockIdx.y * kJoinRows + (tid >> 5);
+    if (meta.r < 0 || row >= meta.rows) return;
     const int64_t size = int64_t(D + 2) * p.part_rows;   // of a part
     const int count = meta.last - c + 1;
-    const float *own = p.parts + int64_t(2 * c + 1) * size, *more = p.parts + int64_t(2 * c + 2) * size;   // then every second
+    const float *own = p.parts + int64_t(2 * c + 1) * size, *more = own + size;    // the first, then every second
     auto part = [&](int k) { return k ? more + int64_t(2 * (k - 1)) * size : own; };
-    auto place = [&](int row) {                          // the row's place in out / D and in lse
-        const int rr = meta.mt * kRows + row, i = rr / p.G;
-        return (int64_t(meta.r) * p.N + i) * p.Hq + meta.h * p.G + (rr - i * p.G);
-    };
-    {
-        const int row = row0 + (tid >> 5);               // a warp per row
-        if (row < meta.rows) {
-            float big = -INFINITY, sum = 0.0f;
-            for (int k = lane; k < count; k += 32) {
-                const float mk = part(k)[D * p.part_rows + row], sk = part(k)[(D + 1) * p.part_rows + row];
-                weight[tid >> 5][k] = sk == 0.0f ? -INFINITY : mk;       // a part the row sees nothing of
-                if (sk != 0.0f) big = fmaxf(big, mk);
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-            for (int k = lane; k < count; k += 32) {
-                const float mk = weight[tid >> 5][k];
-                const float w = mk == -INFINITY ? 0.0f : exp2f((mk - big) * p.c);
-                weight[tid >> 5][k] = w;
-                if (w != 0.0f) sum += w * part(k)[(D + 1) * p.part_rows + row];
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (lane == 0) {
-                s_inv[tid >> 5] = sum == 0.0f ? 0.0f : 1.0f / sum;
-                if (p.lse)
-                    p.lse[place(row)] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(sum));
-            }
-        }
+    float *weight = weights[tid >> 5];
+    float big = -INFINITY, sum = 0.0f;
+    for (int k = lane; k < count; k += 32) {
+        const float mk = part(k)[D * p.part_rows + row], sk = part(k)[(D + 1) * p.part_rows + row];
+        weight[k] = sk == 0.0f ? -INFINITY : mk;         // a part the row sees nothing of
+        if (sk != 0.0f) big = fmaxf(big, mk);
     }
-    __syncthreads();
-    for (int x = tid; x < kJoinRows * D; x += kJoinThreads) {
-        const int y = x % kJoinRows, row = row0 + y, col = x / kJoinRows;
-        if (row >= meta.rows) continue;
-        float o = 0.0f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+    for (int k = lane; k < count; k += 32) {
+        const float mk = weight[k];
+        const float w = mk == -INFINITY ? 0.0f : exp2f((mk - big) * p.c);
+        weight[k] = w;
+        if (w != 0.0f) sum += w * part(k)[(D + 1) * p.part_rows + row];
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    __syncwarp();
+    float o[E] = {};
 #pragma unroll 8
-        for (int k = 0; k < count; ++k) {
-            const float w = weight[y][k], v = part(k)[col * p.part_rows + row];
-            o += w == 0.0f ? 0.0f : w * v;
+    for (int k = 0; k < count; ++k) {
+        const float w = weight[k];
+        const float2 *src = reinterpret_cast<const float2 *>(part(k) + row * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+            const float2 v = src[e];
+            o[2 * e] += w == 0.0f ? 0.0f : w * v.x;
+            o[2 * e + 1] += w == 0.0f ? 0.0f : w * v.y;
         }
-        static_cast<T *>(p.out)[place(row) * D + col] = T(o * s_inv[y]);
     }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int rr = meta.mt * kRows + row, i = rr / p.G;
+    const int64_t o_row = (int64_t(meta.r) * p.N + i) * p.Hq + meta.h * p.G + (rr - i * p.G);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + o_row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) dst[e] = sum == 0.0f ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv, T());
+    if (lane == 0 && p.lse)
+        p.lse[o_row] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(sum));
 }
 
 // -------------------------------------------------------------------- host ----
@@ -812,7 +814,8 @@ int cuda_fail(cudaError_t e, const char *what) { return lookup_record_cuda_error
 // CTAs of a call: as many as run at once on the device.
 int ctas_for(int D, int sms) { return sms * (D == 256 ? 1 : 2); }
 
-int part_rows_for(int64_t N, int64_t G) { return int(N * G < kRows ? N * G : kRows); }
+// Rows of a part: even, so that every part's rows are 16-byte aligned.
+int part_rows_for(int64_t N, int64_t G) { return int(N * G < kRows ? (N * G + 1) / 2 * 2 : kRows); }
 
 size_t workspace_for(int32_t N, int32_t G, int32_t D) {
     const size_t ctas = size_t(ctas_for(D, kMaxSms));
