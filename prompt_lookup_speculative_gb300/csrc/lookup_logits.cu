@@ -1,10 +1,16 @@
 // lookup_logits.cu -- verification of proposal blocks against the target's logits.
 //
-// The contract is in include/lookup_target.h (lookup_verify_logits).  Two kernels:
-// stats_kernel reads every row of logits once and leaves, per row segment, the
-// running maximum m, s = sum exp((x - m) / T) and the lowest index of m;
-// pick_kernel joins a request's segments, finds its first rejected position and
-// draws that row's token.
+// The contract is in include/lookup_target.h (lookup_verify_logits).  What bounds it:
+// the logits' bytes, each row of 0.3 to 0.6 MB read once.  Two kernels:
+// stats_kernel streams every row that a proposal is tested in, cut into segments so
+// that a few rows fill the device, and leaves per segment the running maximum m,
+// s = sum exp((x - m) / T) and (greedy requests) the lowest index of m.
+// pick_kernel, a cluster of CTAs per request, joins a request's segments, finds its
+// first rejected position and reads that one row again, with the noise, for the race
+// that draws its token.  The race needs p(t) - q(t) and so the whole row's sum
+// before its first comparison; a second look at one row of P + 1 is cheaper than
+// carrying every row's race through the first pass, where it would read the noise
+// P + 1 times and double the instructions per logit.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
@@ -17,6 +23,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 namespace {
 
@@ -26,8 +33,13 @@ using lkd::launch_pdl;
 using lkd::wait_for_prerequisite_grid;
 
 constexpr int kStatThreads = 256;
+constexpr int kUnroll = 4;               // 16-byte loads in flight per thread, and as many ahead
 constexpr int kPickThreads = 512;
+constexpr int kKept = 32;                // positions whose statistics a CTA of pick_kernel keeps
+constexpr int kMaxCluster = 8;           // CTAs per request in pick_kernel at most
+constexpr int kRace = 8;                 // logits in flight per thread there
 constexpr int kMaxSegs = 64;             // segments of a row at most
+constexpr int kSegMin = 8192, kSegMax = 32768;   // logits of a segment (where kMaxSegs allows)
 constexpr int kMaxV = 1 << 30;
 
 struct Params {
@@ -37,7 +49,7 @@ struct Params {
     const float *noise, *temperature, *u, *qprobs;
     int64_t qb, qp;                      // strides of qprobs
     const int32_t *point_mass;
-    int32_t B, P, V, segs;
+    int32_t B, P, V, segs, cluster;
     int32_t *out_accepted, *out_commit, *out_ncommit;
     float *out_logprobs;
     float4 *part;                        // [B][P + 1][segs]: m, s, index of m (bits), unused
@@ -102,8 +114,43 @@ __device__ inline Stat warp_join(Stat v, float inv_t) {
     return v;
 }
 
+// 16 bytes of logits as float32.
+__device__ inline void unpack(const uint4 &v, float (&x)[4], float) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+}
+__device__ inline void unpack(const uint4 &v, float (&x)[8], __nv_bfloat16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+__device__ inline void unpack(const uint4 &v, float (&x)[8], __half) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+    }
+}
+
+__device__ inline float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One segment of one row per CTA.  The row is taken in aligned pieces of 16 bytes
+// (the first and the last may be part of the row only), kUnroll of them per thread
+// and pass, the next pass's loads issued before this pass's sums.  Per pass the
+// maximum first, then one factor for the sum so far, then the weights as
+// 2^((x - m) log2(e) / T): the difference before the product, because a product
+// m log2(e) / T, rounded, would shift every weight of the row by up to 3e-6.
 template <typename T>
-__global__ void __launch_bounds__(kStatThreads) stats_kernel(Params p) {
+__global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const __grid_constant__ Params p) {
+    constexpr int E = 16 / int(sizeof(T));               // logits of a piece
     __shared__ Stat warp_stat[kStatThreads / 32];
     wait_for_prerequisite_grid();
     allow_dependent_launch();
@@ -113,18 +160,72 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(Params p) {
     const int n = p.len[b];
     if (i > n || n > p.P) return;                       // a row no proposal is tested in
     const T *row = static_cast<const T *>(p.logits) + b * p.lb + i * p.lp;
+    const bool greedy = is_greedy(p, b);
     const float inv_t = inv_temperature(p, b);
-    const int lo = int(int64_t(p.V) * seg / p.segs), hi = int(int64_t(p.V) * (seg + 1) / p.segs);
-    Stat v{-INFINITY, 0.0f, INT32_MAX};
-    for (int j = lo + threadIdx.x; j < hi; j += kStatThreads) {
-        const float x = logit(row, j);
-        if (x > v.m) {
-            v.s = v.m == -INFINITY ? 1.0f : v.s * weight(v.m, x, inv_t) + 1.0f;
-            v.m = x;
-            v.at = j;
-        } else if (x != -INFINITY) {
-            v.s += weight(x, v.m, inv_t);
+    const float c = inv_t * 1.4426950408889634f;
+    const int mis = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));   // logits before the row in piece 0
+    const int pieces = (p.V + mis + E - 1) / E;
+    const int lo = int(int64_t(pieces) * seg / p.segs), hi = int(int64_t(pieces) * (seg + 1) / p.segs);
+    const uint4 *base = reinterpret_cast<const uint4 *>(row - mis);
+    const uint32_t none = std::is_same<T, float>::value ? 0xff800000u
+                          : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+
+    auto load = [&](int k) -> uint4 {
+        if (k >= hi) return make_uint4(none, none, none, none);
+        if (k * E >= mis && (k + 1) * E - mis <= p.V) return __ldcs(base + k);
+        union {                                          // a piece that is part of the row only
+            uint4 v;
+            T x[E];
+        } u;
+        u.v = make_uint4(none, none, none, none);
+        for (int e = 0; e < E; ++e) {
+            const int j = k * E + e - mis;
+            if (j >= 0 && j < p.V) u.x[e] = row[j];
         }
+        return u.v;
+    };
+
+    Stat v{-INFINITY, 0.0f, INT32_MAX};
+    uint4 next[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) next[k] = load(lo + int(threadIdx.x) + k * kStatThreads);
+    for (int k0 = lo + int(threadIdx.x); k0 < hi; k0 += kUnroll * kStatThreads) {
+        float x[kUnroll][E];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) unpack(next[k], x[k], T());
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) next[k] = load(k0 + (kUnroll + k) * kStatThreads);
+        float big = -INFINITY;                           // (a NaN loses to any number)
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+            for (int e = 0; e < E; ++e) big = fmaxf(big, x[k][e]);
+        if (big > v.m) {
+            v.s = v.m == -INFINITY ? 0.0f : v.s * weight(v.m, big, inv_t);
+            v.m = big;
+            if (greedy) {
+#pragma unroll
+                for (int k = kUnroll - 1; k >= 0; --k)
+#pragma unroll
+                    for (int e = E - 1; e >= 0; --e)
+                        if (x[k][e] == big) v.at = (k0 + k * kStatThreads) * E + e - mis;
+            }
+        }
+        float s[4] = {};
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[e & 3] += exp2_approx((x[k][e] - v.m) * c);
+        float sum = (s[0] + s[1]) + (s[2] + s[3]);
+        if (!(sum <= FLT_MAX)) {                         // infinities or NaN among them: one by one
+            sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (x[k][e] > -INFINITY) sum += weight(x[k][e], v.m, inv_t);
+        }
+        v.s += sum;
     }
     v = warp_join(v, inv_t);
     if ((threadIdx.x & 31) == 0) warp_stat[threadIdx.x >> 5] = v;
@@ -169,19 +270,43 @@ __device__ inline Best warp_better(Best v) {
     return v;
 }
 
-// One CTA per request.
+__device__ inline uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ inline void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ inline void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Writes 8 bytes to the same shared-memory place of the cluster's CTA 0.
+__device__ inline void store_to_first(void *place, uint64_t v) {
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(lkd::smem_addr(place)));
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+__device__ inline uint64_t pack(const Best &b) {
+    return (uint64_t(__float_as_uint(b.key)) << 32) | uint32_t(b.at);
+}
+__device__ inline Best unpack(uint64_t v) { return Best{__uint_as_float(uint32_t(v >> 32)), int32_t(uint32_t(v))}; }
+
+// One cluster per request.  Every CTA of it finds the first rejected position a (a
+// warp per position: its segments joined, its proposal tested), then takes an equal
+// part of row a's race, logit by logit across the threads (noise, q and the row have
+// alignments of their own); CTA 0 takes the best and writes the outputs.
 template <typename T>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(Params p) {
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ Params p) {
     __shared__ int s_first;
-    __shared__ Stat s_row;
+    __shared__ Stat kept[kKept], s_row;
     __shared__ Best warp_res[kPickThreads / 32], warp_all[kPickThreads / 32];
+    __shared__ uint64_t cta_res[kMaxCluster], cta_all[kMaxCluster];
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / p.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = int(cluster_rank());
     const int P = p.P, n = p.len[b];
     int32_t *commit = p.out_commit + int64_t(b) * (P + 1);
     float *lps = p.out_logprobs ? p.out_logprobs + int64_t(b) * (P + 1) : nullptr;
     if (n < 0 || n > P) {                               // no valid block: an error row
+        if (rank) return;
         for (int i = tid; i <= P; i += kPickThreads) {
             commit[i] = -1;
             if (lps) lps[i] = 0.0f;
@@ -193,34 +318,35 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Params p) {
         return;
     }
     const bool greedy = is_greedy(p, b);
+    if (greedy && rank) return;                          // no race: CTA 0 does it all
     const float inv_t = inv_temperature(p, b);
     const T *rows = static_cast<const T *>(p.logits) + b * p.lb;
     const int32_t *block = p.block + int64_t(b) * P;
     if (tid == 0) s_first = n;
     __syncthreads();
     // a warp per position: is its proposal accepted, and with which probability
-    for (int i = warp; i < n; i += kPickThreads / 32) {
+    for (int i = warp; i <= n; i += kPickThreads / 32) {
+        const int d = i < n ? block[i] : -1;
+        const float u = i < n && !greedy ? p.u[int64_t(b) * P + i] : 1.0f;
+        const bool point = !p.qprobs || (i < n && p.point_mass && p.point_mass[int64_t(b) * P + i] != 0);
+        const bool in = d >= 0 && d < p.V;
+        const float x = in ? logit(rows + i * p.lp, d) : -INFINITY;
+        const float q = point || !in ? 1.0f : p.qprobs[b * p.qb + i * p.qp + d];
         const Stat v = row_stat(p, b, i, inv_t, lane);
-        const int d = block[i];
-        const bool fits = d >= 0 && d < p.V && v.m > -INFINITY;
-        const float x = fits ? logit(rows + i * p.lp, d) : -INFINITY;
-        bool ok;
-        if (greedy) {
-            ok = fits && d == v.at;
-        } else {
-            const float pd = fits ? weight(x, v.m, inv_t) / v.s : 0.0f;
-            const bool point = !p.qprobs || (p.point_mass && p.point_mass[int64_t(b) * P + i] != 0);
-            const float q = point || !fits ? 1.0f : p.qprobs[b * p.qb + i * p.qp + d];
-            ok = __fmul_rn(p.u[int64_t(b) * P + i], q) < pd;
-        }
+        if (lane == 0 && i < kKept) kept[i] = v;
+        if (i == n) break;                               // past the block: nothing to test
+        const bool fits = in && v.m > -INFINITY;
+        const bool ok = greedy ? fits && d == v.at : __fmul_rn(u, q) < (fits ? weight(x, v.m, inv_t) / v.s : 0.0f);
         if (lane == 0) {
             if (!ok) atomicMin(&s_first, i);
-            if (lps) lps[i] = ok ? (x == v.m ? 0.0f : (x - v.m) * inv_t) - logf(v.s) : 0.0f;
+            if (lps && !rank) lps[i] = ok ? (x == v.m ? 0.0f : (x - v.m) * inv_t) - logf(v.s) : 0.0f;
         }
     }
     __syncthreads();
     const int a = s_first;
-    if (warp == 0) {
+    if (a < kKept) {
+        if (tid == 0) s_row = kept[a];
+    } else if (warp == 0) {
         const Stat v = row_stat(p, b, a, inv_t, lane);
         if (lane == 0) s_row = v;
     }
@@ -228,19 +354,42 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Params p) {
     const Stat row = s_row;
     const T *x = rows + a * p.lp;
     int32_t token = row.m > -INFINITY ? row.at : -1;
-    if (!greedy && token >= 0) {
+    if (!greedy) {
         // the race: the residual's best key, and p's own for a residual of nothing
+        // (keys without the common factor 1 / s where no q is taken off)
+        cluster_arrive();                                // CTA 0 runs before another writes to it
         const bool rejected = a < n;
-        const bool point = !p.qprobs || (p.point_mass && rejected && p.point_mass[int64_t(b) * P + a] != 0);
+        const bool point = !p.qprobs || (rejected && p.point_mass && p.point_mass[int64_t(b) * P + a] != 0);
         const int32_t d = rejected && point ? block[a] : -1;
         const float *q = rejected && !point ? p.qprobs + b * p.qb + a * p.qp : nullptr;
         const float *noise = p.noise + int64_t(b) * p.V;
+        const int lo = int(int64_t(p.V) * rank / p.cluster), hi = int(int64_t(p.V) * (rank + 1) / p.cluster);
+        const int last = row.m > -INFINITY ? hi : lo;    // an empty row has no race
         Best res{-1.0f, INT32_MAX}, all{-1.0f, INT32_MAX};
-        for (int j = tid; j < p.V; j += kPickThreads) {
-            const float pj = weight(logit(x, j), row.m, inv_t) / row.s, e = noise[j];
-            const float left = j == d ? 0.0f : (q ? pj - q[j] : pj);
-            if (left > 0.0f) res = better(res, Best{left / e, j});
-            if (pj > 0.0f) all = better(all, Best{pj / e, j});
+        for (int j0 = lo + tid; j0 < last; j0 += kRace * kPickThreads) {
+            float xs[kRace], es[kRace], qs[kRace];
+#pragma unroll
+            for (int k = 0; k < kRace; ++k) {
+                const int j = j0 + k * kPickThreads;
+                const bool in = j < last;
+                xs[k] = in ? logit(x, j) : -INFINITY;
+                es[k] = in ? __ldcs(noise + j) : 1.0f;
+                qs[k] = q && in ? __ldcs(q + j) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kRace; ++k) {
+                const int j = j0 + k * kPickThreads;
+                const float w = weight(xs[k], row.m, inv_t);
+                if (q) {
+                    const float pj = w / row.s, left = pj - qs[k];
+                    if (left > 0.0f) res = better(res, Best{left / es[k], j});
+                    if (pj > 0.0f) all = better(all, Best{pj / es[k], j});
+                } else if (w > 0.0f) {
+                    const Best one{w / es[k], j};
+                    if (j != d) res = better(res, one);
+                    else all = one;                      // the refused token, should nothing else be left
+                }
+            }
         }
         res = warp_better(res);
         all = warp_better(all);
@@ -249,12 +398,27 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Params p) {
             warp_all[warp] = all;
         }
         __syncthreads();
+        cluster_wait();
         if (warp == 0) {
             res = lane < kPickThreads / 32 ? warp_res[lane] : Best{-1.0f, INT32_MAX};
             all = lane < kPickThreads / 32 ? warp_all[lane] : Best{-1.0f, INT32_MAX};
             res = warp_better(res);
             all = warp_better(all);
-            token = res.key >= 0.0f ? res.at : all.at;
+            if (lane == 0) {
+                store_to_first(&cta_res[rank], pack(res));
+                store_to_first(&cta_all[rank], pack(all));
+            }
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        if (rank) return;
+        if (warp == 0) {
+            res = lane < p.cluster ? unpack(cta_res[lane]) : Best{-1.0f, INT32_MAX};
+            all = lane < p.cluster ? unpack(cta_all[lane]) : Best{-1.0f, INT32_MAX};
+            res = warp_better(res);
+            all = warp_better(all);
+            token = res.key >= 0.0f ? res.at : (all.key >= 0.0f ? all.at : -1);
         }
     }
     if (warp == 0) {
@@ -276,19 +440,44 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(Params p) {
     }
 }
 
+// Segments of a row: enough CTAs for two waves of stats_kernel where rows are few,
+// at most kSegMax logits each and, where that leaves a choice, at least kSegMin.
 int segments(int32_t B, int32_t P, int32_t V) {
     const int64_t rows = int64_t(B) * (P + 1);
-    int64_t s = 152 * 16 / (rows > 0 ? rows : 1) + 1;
-    const int64_t most = (int64_t(V) + 4095) / 4096;
-    if (s > most) s = most;
+    const int64_t want = 152 * 8 / (rows > 0 ? rows : 1) + 1;
+    const int64_t least = (int64_t(V) + kSegMax - 1) / kSegMax, most = (int64_t(V) + kSegMin - 1) / kSegMin;
+    int64_t s = want < most ? want : most;
+    s = s > least ? s : least;
     return int(s > kMaxSegs ? kMaxSegs : s);
+}
+
+// CTAs of a request's cluster: one per 16384 logits of its race, a power of two.
+int cluster_for(int32_t V) {
+    int c = 1;
+    while (c < kMaxCluster && int64_t(c) * 16384 < V) c *= 2;
+    return c;
 }
 
 template <typename T>
 int launch(const Params &p, cudaStream_t stream) {
     int rc = launch_pdl(stats_kernel<T>, unsigned(int64_t(p.B) * (p.P + 1) * p.segs), unsigned(kStatThreads), stream, p);
     if (rc != LOOKUP_DRAFT_OK) return rc;
-    return launch_pdl(pick_kernel<T>, unsigned(p.B), unsigned(kPickThreads), stream, p);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(p.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(p.B) * unsigned(p.cluster));
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, pick_kernel<T>, p);
+    if (e != cudaSuccess) return lookup_record_cuda_error(e, "kernel launch");
+    lookup_note_launch();
+    return LOOKUP_DRAFT_OK;
 }
 
 bool misaligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
@@ -312,7 +501,7 @@ int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *l
     if (type != LOOKUP_TYPE_F32 && type != LOOKUP_TYPE_F16 && type != LOOKUP_TYPE_BF16) return LOOKUP_DRAFT_EINVAL;
     if (B == 0) return LOOKUP_DRAFT_OK;
     const int segs = segments(B, P, V);
-    if (int64_t(B) * (P + 1) * segs > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
+    if (int64_t(B) * (P + 1) * segs > INT32_MAX || int64_t(B) * kMaxCluster > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
     if ((P > 0 && !block) || !len || !logits || !logits_strides || !out_accepted || !out_commit || !out_ncommit ||
         !workspace)
         return LOOKUP_DRAFT_EINVAL;
@@ -329,7 +518,7 @@ int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *l
     const bool with_q = noise && qprobs && P > 0;
     Params p{block, len, logits, logits_strides[0], logits_strides[1], noise, noise ? temperature : nullptr, u,
              with_q ? qprobs : nullptr, with_q ? qprobs_strides[0] : 0, with_q ? qprobs_strides[1] : 0, point_mass,
-             B, P, V, segs, out_accepted, out_commit, out_ncommit, out_logprobs, static_cast<float4 *>(workspace)};
+             B, P, V, segs, cluster_for(V), out_accepted, out_commit, out_ncommit, out_logprobs, static_cast<float4 *>(workspace)};
     if (type == LOOKUP_TYPE_F32) return launch<float>(p, stream);
     if (type == LOOKUP_TYPE_F16) return launch<__half>(p, stream);
     return launch<__nv_bfloat16>(p, stream);
