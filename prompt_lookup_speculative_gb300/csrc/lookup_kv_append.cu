@@ -1,7 +1,12 @@
 // lookup_kv_append.cu -- rotary positions and the append to the paged cache.
 //
-// The contract is in include/lookup_target.h (lookup_kv_append).  One kernel, one
-// thread per (token, head, rotated pair or copied pair of elements).
+// The contract is in include/lookup_target.h (lookup_kv_append).  What bounds it: the
+// bytes of q, k and v, read once and written once.  One launch: each thread takes one
+// unit of 16 elements of a head (for a rotated unit, the 8 pairs that share 8
+// angles) for up to kHeads heads of one token, so the angles are read once for them
+// and all their 16-byte loads are in flight together.  Sizes, strides or addresses
+// that are not multiples of 16 bytes take a kernel of one pair of elements per thread.
+// The last CTAs of either kernel report the requests with tokens that have no slot.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
@@ -20,6 +25,7 @@ using lkd::launch_pdl;
 using lkd::wait_for_prerequisite_grid;
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;                // heads of a thread
 constexpr int kMaxD = 1024;
 
 struct Strides {
@@ -34,6 +40,8 @@ struct Params {
     void *k_cache, *v_cache, *out_q;
     int32_t *status;
     int32_t B, N, Hq, Hkv, D, max_pages, pages, page_shift, rot, max_pos, interleaved;
+    int32_t tokens;                      // of a CTA of append_units_kernel
+    int32_t grid;                        // CTAs that append; the ones after them report
 };
 
 __device__ inline float to_f32(__half x) { return __half2float(x); }
@@ -57,22 +65,141 @@ __device__ inline int64_t slot_of(const Params &p, int b, int64_t pos) {
     return ((int64_t(page) * p.Hkv) << p.page_shift) + (pos & ((int64_t(1) << p.page_shift) - 1));
 }
 
-// 1 where any of the request's tokens has no slot, by its whole block of threads.
-__global__ void status_kernel(Params p) {
-    wait_for_prerequisite_grid();
-    allow_dependent_launch();
-    const int b = blockIdx.x;
-    const int n = block_tokens(p, b);
-    bool bad = false;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) bad |= slot_of(p, b, int64_t(max(p.kv_len[b], 0)) + i) < 0;
-    bad = __syncthreads_or(bad) != 0;
-    if (threadIdx.x == 0) p.status[b] = bad ? 1 : 0;
+// status, by the CTAs after the appending ones: a warp per request, which looks at
+// each page that the block's tokens touch.
+__device__ inline void report(const Params &p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t b = int64_t(blockIdx.x - p.grid) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (b >= p.B) return;
+    const int n = block_tokens(p, int(b));
+    const int64_t first = max(p.kv_len[b], 0), end = first + n;
+    bool bad = n > 0 && p.rotary && end > p.max_pos;
+    if (n > 0)
+        for (int64_t at = (first >> p.page_shift) + lane; at <= ((end - 1) >> p.page_shift); at += 32) {
+            const int32_t page = at < p.max_pages ? p.table[b * p.max_pages + at] : -1;
+            bad |= page < 0 || page >= p.pages;
+        }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) p.status[b] = bad ? 1 : 0;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(Params p) {
+__device__ inline float2 unpack2(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+__device__ inline float2 unpack2(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ inline uint32_t pack2(float lo, float hi, __half) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ inline uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Two words of a pair's unit rotated.  Half layout: x holds two a, y the two b that
+// pair with them.  Interleaved: x and y each hold one pair.
+template <typename T, bool INTER>
+__device__ inline void turn(uint32_t &x, uint32_t &y, float c0, float s0, float c1, float s1) {
+    const float2 f = unpack2(x, T()), g = unpack2(y, T());
+    if (INTER) {
+        x = pack2(f.x * c0 - f.y * s0, f.y * c0 + f.x * s0, T());
+        y = pack2(g.x * c1 - g.y * s1, g.y * c1 + g.x * s1, T());
+    } else {
+        x = pack2(f.x * c0 - g.x * s0, f.y * c1 - g.y * s1, T());
+        y = pack2(g.x * c0 + f.x * s0, g.y * c1 + f.y * s1, T());
+    }
+}
+
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads) append_units_kernel(const __grid_constant__ Params p) {
     wait_for_prerequisite_grid();
     allow_dependent_launch();
+    if (int(blockIdx.x) >= p.grid) return report(p);
+    const int units = p.D / 16;
+    const int q_groups = p.q ? (p.Hq + kHeads - 1) / kHeads : 0, k_groups = p.k ? (p.Hkv + kHeads - 1) / kHeads : 0;
+    const int groups = q_groups + 2 * k_groups;
+    const int64_t tok0 = int64_t(blockIdx.x) * p.tokens;
+    const int b0 = int(tok0 / p.N), i0 = int(tok0 - int64_t(b0) * p.N);
+    for (int x = threadIdx.x; x < p.tokens * units * groups; x += kThreads) {
+        const int t = x / (units * groups);
+        const int u = x % units;                         // neighbouring threads: neighbouring units of a head
+        int g = x / units - t * groups;
+        const int b = b0 + (i0 + t) / p.N, i = (i0 + t) % p.N;
+        if (b >= p.B) return;
+        const bool is_q = g < q_groups, is_k = !is_q && g < q_groups + k_groups;
+        if (!is_q) g -= is_k ? q_groups : q_groups + k_groups;
+        const int h0 = g * kHeads, heads = min(kHeads, (is_q ? p.Hq : p.Hkv) - h0);
+        const bool inside = i < block_tokens(p, b);
+        if (!inside && !is_q) continue;
+        const int64_t pos = int64_t(max(p.kv_len[b], 0)) + i;
+        const bool turned = u < p.rot / 16 && (is_q || is_k);
+        // the unit's two 16-byte parts in a head
+        int e0 = 16 * u, e1 = 16 * u + 8;
+        if (!INTER && u < p.rot / 16) {
+            e0 = 8 * u;
+            e1 = p.rot / 2 + 8 * u;
+        }
+        uint4 v0[kHeads], v1[kHeads];
+        if (inside) {
+            const Strides &st = is_q ? p.qs : is_k ? p.ks : p.vs;
+            const T *src = static_cast<const T *>(is_q ? p.q : is_k ? p.k : p.v) + b * st.b + i * st.n + h0 * st.h;
+#pragma unroll
+            for (int k = 0; k < kHeads; ++k)
+                if (k < heads) {
+                    v0[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * st.h + e0));
+                    v1[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * st.h + e1));
+                }
+        }
+        const int64_t slot = inside ? slot_of(p, b, pos) : -1;
+        T *dst;
+        int64_t step;
+        if (is_q) {
+            dst = static_cast<T *>(p.out_q) + ((int64_t(b) * p.N + i) * p.Hq + h0) * p.D;
+            step = p.D;
+        } else {
+            if (slot < 0) continue;
+            dst = static_cast<T *>(is_k ? p.k_cache : p.v_cache) + (slot + (int64_t(h0) << p.page_shift)) * p.D;
+            step = int64_t(p.D) << p.page_shift;
+        }
+        if (slot < 0) {                                  // a query row past the block, or without a slot
+#pragma unroll
+            for (int k = 0; k < kHeads; ++k) v0[k] = v1[k] = make_uint4(0, 0, 0, 0);
+        } else if (turned) {
+            const float *row = p.rotary + pos * p.rot + 8 * u;
+            const float4 c0 = *reinterpret_cast<const float4 *>(row), c1 = *reinterpret_cast<const float4 *>(row + 4);
+            const float4 s0 = *reinterpret_cast<const float4 *>(row + p.rot / 2);
+            const float4 s1 = *reinterpret_cast<const float4 *>(row + p.rot / 2 + 4);
+#pragma unroll
+            for (int k = 0; k < kHeads; ++k)
+                if (k < heads) {
+                    if (INTER) {                         // words of pairs 0 .. 3, then 4 .. 7
+                        turn<T, INTER>(v0[k].x, v0[k].y, c0.x, s0.x, c0.y, s0.y);
+                        turn<T, INTER>(v0[k].z, v0[k].w, c0.z, s0.z, c0.w, s0.w);
+                        turn<T, INTER>(v1[k].x, v1[k].y, c1.x, s1.x, c1.y, s1.y);
+                        turn<T, INTER>(v1[k].z, v1[k].w, c1.z, s1.z, c1.w, s1.w);
+                    } else {                             // words of a and of b, two pairs each
+                        turn<T, INTER>(v0[k].x, v1[k].x, c0.x, s0.x, c0.y, s0.y);
+                        turn<T, INTER>(v0[k].y, v1[k].y, c0.z, s0.z, c0.w, s0.w);
+                        turn<T, INTER>(v0[k].z, v1[k].z, c1.x, s1.x, c1.y, s1.y);
+                        turn<T, INTER>(v0[k].w, v1[k].w, c1.z, s1.z, c1.w, s1.w);
+                    }
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k)
+            if (k < heads) {
+                *reinterpret_cast<uint4 *>(dst + k * step + e0) = v0[k];
+                *reinterpret_cast<uint4 *>(dst + k * step + e1) = v1[k];
+            }
+    }
+}
+
+// One pair of elements of one head per thread.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) append_pairs_kernel(const __grid_constant__ Params p) {
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    if (int(blockIdx.x) >= p.grid) return report(p);
     const int half_d = (p.D + 1) / 2;
     const int heads = (p.q ? p.Hq : 0) + (p.k ? 2 * p.Hkv : 0);
     const int64_t idx = int64_t(blockIdx.x) * kThreads + threadIdx.x;
@@ -162,17 +289,35 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
     p.B = B, p.N = N, p.Hq = Hq, p.Hkv = Hkv, p.D = D, p.max_pages = max_pages, p.pages = pages;
     while ((1 << p.page_shift) < page_size) ++p.page_shift;
     p.rot = rotary ? rot : 0, p.max_pos = max_pos, p.interleaved = interleaved;
+    // whole 16-byte accesses everywhere: sizes, strides and addresses allow them
+    bool units = D % 16 == 0 && p.rot % 16 == 0;
+    for (const Strides *st : {&p.qs, &p.ks, &p.vs}) units = units && !((st->b | st->n | st->h) & 7);
+    for (const void *x : {q, k, v, static_cast<const void *>(k_cache), static_cast<const void *>(v_cache),
+                          static_cast<const void *>(out_q), static_cast<const void *>(rotary)})
+        units = units && !misaligned(x, 16);
+    int64_t grid = 0;
     if (q || k) {
-        const int64_t threads = int64_t(B) * N * ((q ? Hq : 0) + (k ? 2 * Hkv : 0)) * ((D + 1) / 2);
-        const int64_t grid = (threads + kThreads - 1) / kThreads;
-        if (grid > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
-        const int rc = type == LOOKUP_TYPE_F16
-                           ? launch_pdl(append_kernel<__half>, unsigned(grid), unsigned(kThreads), stream, p)
-                           : launch_pdl(append_kernel<__nv_bfloat16>, unsigned(grid), unsigned(kThreads), stream, p);
-        if (rc != LOOKUP_DRAFT_OK) return rc;
+        if (units) {
+            const int groups = (q ? (Hq + kHeads - 1) / kHeads : 0) + (k ? 2 * ((Hkv + kHeads - 1) / kHeads) : 0);
+            const int64_t per = int64_t(groups) * (D / 16);          // threads of a token
+            if (per > INT32_MAX / kThreads) return LOOKUP_DRAFT_EINVAL;
+            p.tokens = per < kThreads ? int32_t(kThreads / per) : 1;
+            grid = (int64_t(B) * N + p.tokens - 1) / p.tokens;
+        } else {
+            const int64_t heads = (q ? int64_t(Hq) : 0) + (k ? 2 * int64_t(Hkv) : 0);
+            if (int64_t(B) * N > (int64_t(1) << 40) / heads) return LOOKUP_DRAFT_EINVAL;
+            grid = (int64_t(B) * N * heads * ((D + 1) / 2) + kThreads - 1) / kThreads;
+        }
     }
-    if (status) return launch_pdl(status_kernel, unsigned(B), unsigned(kThreads), stream, p);
-    return LOOKUP_DRAFT_OK;
+    const int64_t all = grid + (status ? (int64_t(B) + kThreads / 32 - 1) / (kThreads / 32) : 0);
+    if (all > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
+    if (all == 0) return LOOKUP_DRAFT_OK;
+    p.grid = int32_t(grid);
+    const bool half = type == LOOKUP_TYPE_F16;
+    auto kernel = units ? (interleaved ? (half ? append_units_kernel<__half, true> : append_units_kernel<__nv_bfloat16, true>)
+                                       : (half ? append_units_kernel<__half, false> : append_units_kernel<__nv_bfloat16, false>))
+                        : (half ? append_pairs_kernel<__half> : append_pairs_kernel<__nv_bfloat16>);
+    return launch_pdl(kernel, unsigned(all), unsigned(kThreads), stream, p);
 }
 
 }  // extern "C"
