@@ -239,7 +239,7 @@ def _check(rc: int, lib) -> None:
 def _stream_handle(stream) -> int:
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream)
 
 
@@ -440,7 +440,7 @@ def _dev(t, dtype, shape, device, name, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
@@ -936,12 +936,13 @@ class ContextCache:
 
 
 # ------------------------------------------- the target's side of a verify step ----
-_TYPES = {"float32": 0, "float16": 1, "bfloat16": 2}      # LOOKUP_TYPE_* of include/lookup_target.h
+_TYPES = {"torch.float32": 0, "torch.float16": 1, "torch.bfloat16": 2}      # LOOKUP_TYPE_* of include/lookup_target.h
+_Strides = {n: ctypes.c_int64 * n for n in (2, 3)}
 
 
-def _type_code(t, name, allowed):
-    code = _TYPES.get(str(t.dtype).removeprefix("torch."))
-    if code is None or code not in allowed:
+def _type_code(t, name, least=0):
+    code = _TYPES.get(str(t.dtype), -1)
+    if code < least:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
     return code
 
@@ -949,20 +950,30 @@ def _type_code(t, name, allowed):
 def _strided(t, shape, dtype, device, name):
     """Check a device tensor whose last axis is dense and whose other strides are free;
     return its pointer and the C array of those strides."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    if t.dtype != dtype or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}")
     st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be dense")
-    if any(x < 0 for x in st):
-        raise ValueError(f"{name}: negative strides")
-    return t.data_ptr(), (ctypes.c_int64 * (len(shape) - 1))(*st[:-1])
+    return t.data_ptr(), _Strides[len(shape) - 1](*st[:-1])
 
 
 def _cuda_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.device
+
+
+def _call(fn, dev, stream, *args):
+    """Run an entry point on the device, its stream last."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream_handle(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream_handle(stream))
+    if rc:
+        raise LookupDraftError(rc, load_library())
 
 
 def _scratch(nbytes, workspace, device, stream):
@@ -1043,44 +1054,41 @@ def _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, dtype, dev):
     return pages, hkv, page, mp, ptrs
 
 
-def lookup_kv_append(q, k, v, kv_len, block_table, k_cache, v_cache, rotary=None, rot=None, q_len=None,
+def lookup_kv_append(q, k, v, kv_len, block_table, k_cache, v_cache, rotary=None, q_len=None,
                      interleaved: bool = False, out_q=None, status=None, stream=None):
     """Rotate a verify block's queries and keys and write its keys and values to the paged
     cache [pages, Hkv, page_size, D] (include/lookup_target.h).  q [B, N, Hq, D], k and
     v [B, N, Hkv, D] may be strided views; ``rotary`` is rotary_table's [max_pos, rot].
     Returns (rotated q [B, N, Hq, D], status [B]: 1 where a token had no slot)."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _cuda_device(q, "q")
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q and k must be [B, N, heads, D]")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, Hq, D]")
     B, N, hq, D = q.shape
-    code = _type_code(q, "q", (1, 2))
-    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, q.dtype, dev)
-    qp, qs = _strided(q, (B, N, hq, D), q.dtype, dev, "q")
-    kp, ks = _strided(k, (B, N, hkv, D), q.dtype, dev, "k")
-    vp, vs = _strided(v, (B, N, hkv, D), q.dtype, dev, "v")
-    rp, max_pos = None, 0
+    dtype, code = q.dtype, _type_code(q, "q", 1)
+    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, dtype, dev)
+    qp, qs = _strided(q, (B, N, hq, D), dtype, dev, "q")
+    kp, ks = _strided(k, (B, N, hkv, D), dtype, dev, "k")
+    vp, vs = _strided(v, (B, N, hkv, D), dtype, dev, "v")
+    rp, max_pos, rot = None, 0, 0
     if rotary is not None:
         if rotary.dim() != 2:
             raise ValueError("rotary must be [max_pos, rot]")
-        max_pos, width = rotary.shape
-        if rot is not None and rot != width:
-            raise ValueError("rot differs from the table's width")
-        rot = width
-        rp = _dev(rotary, torch.float32, (max_pos, width), dev, "rotary")
+        max_pos, rot = rotary.shape
+        rp = _dev(rotary, torch.float32, (max_pos, rot), dev, "rotary")
     if out_q is None:
-        out_q = torch.empty((B, N, hq, D), dtype=q.dtype, device=dev)
+        out_q = torch.empty((B, N, hq, D), dtype=dtype, device=dev)
+    else:
+        _dev(out_q, dtype, (B, N, hq, D), dev, "out_q")
     if status is None:
         status = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _dev(status, torch.int32, (B,), dev, "status")
     if N == 0:
         status.zero_()
-    op = _dev(out_q, q.dtype, (B, N, hq, D), dev, "out_q")
-    sp = _dev(status, torch.int32, (B,), dev, "status")
-    with torch.cuda.device(dev):
-        rc = lib.lookup_kv_append(qp, qs, kp, ks, vp, vs, kl, ql, bt, B, N, hq, hkv, D, mp, pages, page, rp, rot or 0,
-                                  max_pos, 1 if interleaved else 0, code, kc, vc, op, sp, _stream_handle(stream))
-    _check(rc, lib)
+    _call(lib.lookup_kv_append, dev, stream, qp, qs, kp, ks, vp, vs, kl, ql, bt, B, N, hq, hkv, D, mp, pages, page, rp,
+          rot, max_pos, 1 if interleaved else 0, code, kc, vc, out_q.data_ptr(), status.data_ptr())
     return out_q, status
 
 
@@ -1091,26 +1099,25 @@ def lookup_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None,
     kv_len[r] + i.  ``scale`` defaults to D**-0.5; ``window`` > 0 limits each token to
     itself and the window - 1 before it.  Returns (out [B, N, Hq, D], lse float32 [B, N, Hq])."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _cuda_device(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be [B, N, Hq, D]")
     B, N, hq, D = q.shape
-    code = _type_code(q, "q", (1, 2))
-    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, q.dtype, dev)
-    qp, qs = _strided(q, (B, N, hq, D), q.dtype, dev, "q")
+    dtype, code = q.dtype, _type_code(q, "q", 1)
+    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, dtype, dev)
+    qp, qs = _strided(q, (B, N, hq, D), dtype, dev, "q")
     if out is None:
-        out = torch.empty((B, N, hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty((B, N, hq, D), dtype=dtype, device=dev)
+    else:
+        _dev(out, dtype, (B, N, hq, D), dev, "out")
     if lse is None:
         lse = torch.empty((B, N, hq), dtype=torch.float32, device=dev)
-    op = _dev(out, q.dtype, (B, N, hq, D), dev, "out")
-    lp = _dev(lse, torch.float32, (B, N, hq), dev, "lse")
-    with torch.cuda.device(dev):
-        ws, nbytes = _scratch(lib.lookup_paged_attention_workspace_bytes(B, N, hq, hkv, D), workspace, dev, stream)
-        rc = lib.lookup_paged_attention(qp, qs, kc, vc, bt, kl, ql, B, N, hq, hkv, D, mp, pages, page,
-                                        D ** -0.5 if scale is None else scale, window, code, op, lp, ws.data_ptr(),
-                                        nbytes, _stream_handle(stream))
-    _check(rc, lib)
+    else:
+        _dev(lse, torch.float32, (B, N, hq), dev, "lse")
+    ws, nbytes = _scratch(lib.lookup_paged_attention_workspace_bytes(B, N, hq, hkv, D), workspace, dev, stream)
+    _call(lib.lookup_paged_attention, dev, stream, qp, qs, kc, vc, bt, kl, ql, B, N, hq, hkv, D, mp, pages, page,
+          D ** -0.5 if scale is None else scale, window, code, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), nbytes)
     return out, lse
 
 
@@ -1123,32 +1130,30 @@ def lookup_verify_logits(block, length, logits, noise=None, u=None, temperature=
     distributions ``qprobs`` [B, P, V] (None = point masses).  Returns (accepted [B],
     commit [B, P + 1], ncommit [B], logprobs float32 [B, P + 1])."""
     import torch
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _cuda_device(logits, "logits")
     if block.dim() != 2 or logits.dim() != 3:
         raise ValueError("block must be [B, P] and logits [B, P + 1, V]")
     B, P = block.shape
     V = logits.shape[2]
     i32, f32 = torch.int32, torch.float32
-    code = _type_code(logits, "logits", (0, 1, 2))
+    code = _type_code(logits, "logits")
     lp, ls = _strided(logits, (B, P + 1, V), logits.dtype, dev, "logits")
     qp, qs = (None, None) if qprobs is None else _strided(qprobs, (B, P, V), f32, dev, "qprobs")
-    args = (_dev(noise, f32, (B, V), dev, "noise", optional=True),
-            _dev(temperature, f32, (B,), dev, "temperature", optional=True),
-            _dev(u, f32, (B, P), dev, "u", optional=noise is None))
-    bp, np_ = _dev(block, i32, (B, P), dev, "block"), _dev(length, i32, (B,), dev, "len")
-    pm = _dev(point_mass, i32, (B, P), dev, "point_mass", optional=True)
     if out is None:
         out = (torch.empty(B, dtype=i32, device=dev), torch.empty((B, P + 1), dtype=i32, device=dev),
                torch.empty(B, dtype=i32, device=dev), torch.empty((B, P + 1), dtype=f32, device=dev))
+    else:
+        for t, dtype, shape, name in zip(out, (i32, i32, i32, f32), ((B,), (B, P + 1), (B,), (B, P + 1)),
+                                         ("accepted", "commit", "ncommit", "logprobs"), strict=True):
+            _dev(t, dtype, shape, dev, name)
     acc, commit, nc, lps = out
-    optr = (_dev(acc, i32, (B,), dev, "accepted"), _dev(commit, i32, (B, P + 1), dev, "commit"),
-            _dev(nc, i32, (B,), dev, "ncommit"), _dev(lps, f32, (B, P + 1), dev, "logprobs"))
-    with torch.cuda.device(dev):
-        ws, nbytes = _scratch(lib.lookup_verify_logits_workspace_bytes(B, P, V), workspace, dev, stream)
-        rc = lib.lookup_verify_logits(bp, np_, lp, ls, code, V, *args, qp, qs, pm, B, P, *optr, ws.data_ptr(), nbytes,
-                                      _stream_handle(stream))
-    _check(rc, lib)
+    ws, nbytes = _scratch(lib.lookup_verify_logits_workspace_bytes(B, P, V), workspace, dev, stream)
+    _call(lib.lookup_verify_logits, dev, stream, _dev(block, i32, (B, P), dev, "block"),
+          _dev(length, i32, (B,), dev, "len"), lp, ls, code, V, _dev(noise, f32, (B, V), dev, "noise", True),
+          _dev(temperature, f32, (B,), dev, "temperature", True), _dev(u, f32, (B, P), dev, "u", noise is None), qp, qs,
+          _dev(point_mass, i32, (B, P), dev, "point_mass", True), B, P, acc.data_ptr(), commit.data_ptr(), nc.data_ptr(),
+          lps.data_ptr(), ws.data_ptr(), nbytes)
     return acc, commit, nc, lps
 
 
