@@ -111,7 +111,7 @@ __device__ inline void turn(uint32_t &x, uint32_t &y, float c0, float s0, float 
 }
 
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads) append_units_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 3) append_units_kernel(const __grid_constant__ Params p) {
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     if (int(blockIdx.x) >= p.grid) return report(p);
@@ -129,8 +129,6 @@ __global__ void __launch_bounds__(kThreads) append_units_kernel(const __grid_con
         const bool is_q = g < q_groups, is_k = !is_q && g < q_groups + k_groups;
         if (!is_q) g -= is_k ? q_groups : q_groups + k_groups;
         const int h0 = g * kHeads, heads = min(kHeads, (is_q ? p.Hq : p.Hkv) - h0);
-        const bool inside = i < block_tokens(p, b);
-        if (!inside && !is_q) continue;
         const int64_t pos = int64_t(max(p.kv_len[b], 0)) + i;
         const bool turned = u < p.rot / 16 && (is_q || is_k);
         // the unit's two 16-byte parts in a head
@@ -139,18 +137,17 @@ __global__ void __launch_bounds__(kThreads) append_units_kernel(const __grid_con
             e0 = 8 * u;
             e1 = p.rot / 2 + 8 * u;
         }
+        // the loads first: they wait for nothing (rows past q_len are there, if unused)
         uint4 v0[kHeads], v1[kHeads];
-        if (inside) {
-            const Strides &st = is_q ? p.qs : is_k ? p.ks : p.vs;
-            const T *src = static_cast<const T *>(is_q ? p.q : is_k ? p.k : p.v) + b * st.b + i * st.n + h0 * st.h;
+        const Strides &st = is_q ? p.qs : is_k ? p.ks : p.vs;
+        const T *src = static_cast<const T *>(is_q ? p.q : is_k ? p.k : p.v) + b * st.b + i * st.n + h0 * st.h;
 #pragma unroll
-            for (int k = 0; k < kHeads; ++k)
-                if (k < heads) {
-                    v0[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * st.h + e0));
-                    v1[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * st.h + e1));
-                }
-        }
-        const int64_t slot = inside ? slot_of(p, b, pos) : -1;
+        for (int k = 0; k < kHeads; ++k)
+            if (k < heads) {
+                v0[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * st.h + e0));
+                v1[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * st.h + e1));
+            }
+        const int64_t slot = i < block_tokens(p, b) ? slot_of(p, b, pos) : -1;
         T *dst;
         int64_t step;
         if (is_q) {

@@ -33,13 +33,14 @@ using lkd::launch_pdl;
 using lkd::wait_for_prerequisite_grid;
 
 constexpr int kStatThreads = 256;
-constexpr int kUnroll = 4;               // 16-byte loads in flight per thread, and as many ahead
+constexpr int kUnroll = 8;               // 16-byte loads in flight per thread
 constexpr int kPickThreads = 512;
 constexpr int kKept = 32;                // positions whose statistics a CTA of pick_kernel keeps
 constexpr int kMaxCluster = 8;           // CTAs per request in pick_kernel at most
-constexpr int kRace = 8;                 // logits in flight per thread there
+constexpr int kRace = 16;                // logits in flight per thread there
 constexpr int kMaxSegs = 64;             // segments of a row at most
-constexpr int kSegMin = 8192, kSegMax = 32768;   // logits of a segment (where kMaxSegs allows)
+constexpr int kSegBytes = 4 * kUnroll * kStatThreads * 16;  // of a segment at most: four passes (where kMaxSegs allows)
+constexpr int kSegMin = 8192;            // logits of a segment at least, where there is a choice
 constexpr int kMaxV = 1 << 30;
 
 struct Params {
@@ -102,38 +103,53 @@ __device__ inline Stat join(const Stat &a, const Stat &b, float inv_t) {
     return r;
 }
 
-__device__ inline Stat warp_join(Stat v, float inv_t) {
+// The warp's lanes as one: the maximum first, one factor per lane, then the sum (and
+// the index, where it is wanted); every lane gets the result.
+__device__ inline Stat warp_join(Stat v, float inv_t, bool index) {
+    float m = v.m;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        Stat o;
-        o.m = __shfl_xor_sync(0xffffffffu, v.m, d);
-        o.s = __shfl_xor_sync(0xffffffffu, v.s, d);
-        o.at = __shfl_xor_sync(0xffffffffu, v.at, d);
-        v = join(v, o, inv_t);
-    }
-    return v;
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float s = v.m == -INFINITY ? 0.0f : v.s * weight(v.m, m, inv_t);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    const int32_t at = index ? __reduce_min_sync(0xffffffffu, v.m == m ? v.at : INT32_MAX) : INT32_MAX;
+    return Stat{m, s, at};
 }
 
-// 16 bytes of logits as float32.
-__device__ inline void unpack(const uint4 &v, float (&x)[4], float) {
-    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+// Word k of a piece of 16 bytes as two logits (float32: words 2k and 2k + 1).
+__device__ inline float2 two(const uint4 &v, int k, float) {
+    return k ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w))
+             : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
 }
-__device__ inline void unpack(const uint4 &v, float (&x)[8], __nv_bfloat16) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-    }
+__device__ inline uint32_t word(const uint4 &v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
+__device__ inline float2 two(const uint4 &v, int k, __nv_bfloat16) {
+    return make_float2(__uint_as_float(word(v, k) << 16), __uint_as_float(word(v, k) & 0xffff0000u));
 }
-__device__ inline void unpack(const uint4 &v, float (&x)[8], __half) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
-        x[2 * k] = f.x;
-        x[2 * k + 1] = f.y;
-    }
+__device__ inline float2 two(const uint4 &v, int k, __half) {
+    const uint32_t w = word(v, k);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// The largest logit of two pieces, word by word (a NaN loses to any number).
+__device__ inline uint4 max_words(const uint4 &a, const uint4 &b, float) {
+    return make_uint4(__float_as_uint(fmaxf(__uint_as_float(a.x), __uint_as_float(b.x))),
+                      __float_as_uint(fmaxf(__uint_as_float(a.y), __uint_as_float(b.y))),
+                      __float_as_uint(fmaxf(__uint_as_float(a.z), __uint_as_float(b.z))),
+                      __float_as_uint(fmaxf(__uint_as_float(a.w), __uint_as_float(b.w))));
+}
+__device__ inline uint32_t max_pair(uint32_t a, uint32_t b, __half) {
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ inline uint32_t max_pair(uint32_t a, uint32_t b, __nv_bfloat16) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <typename T>
+__device__ inline uint4 max_words(const uint4 &a, const uint4 &b, T t) {
+    return make_uint4(max_pair(a.x, b.x, t), max_pair(a.y, b.y, t), max_pair(a.z, b.z, t), max_pair(a.w, b.w, t));
 }
 
 __device__ inline float exp2_approx(float x) {
@@ -142,21 +158,39 @@ __device__ inline float exp2_approx(float x) {
     return y;
 }
 
+// Two float32 operations in one instruction.
+__device__ inline float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ inline float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // One segment of one row per CTA.  The row is taken in aligned pieces of 16 bytes
 // (the first and the last may be part of the row only), kUnroll of them per thread
-// and pass, the next pass's loads issued before this pass's sums.  Per pass the
-// maximum first, then one factor for the sum so far, then the weights as
-// 2^((x - m) log2(e) / T): the difference before the product, because a product
-// m log2(e) / T, rounded, would shift every weight of the row by up to 3e-6.
+// and pass, all in flight together; the SM's other CTAs compute meanwhile.  Per pass
+// the maximum first, in the type itself, then one factor for the sum so far, then the
+// weights as 2^((x - m) log2(e) / T): the difference before the product, because a
+// product m log2(e) / T, rounded, would shift every weight of the row by up to 3e-6.
 template <typename T>
-__global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kStatThreads, sizeof(T) == 4 ? 4 : 3) stats_kernel(const __grid_constant__ Params p) {
     constexpr int E = 16 / int(sizeof(T));               // logits of a piece
     __shared__ Stat warp_stat[kStatThreads / 32];
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    const int seg = blockIdx.x % p.segs;
-    const int64_t row_id = blockIdx.x / p.segs;
-    const int b = int(row_id / (p.P + 1)), i = int(row_id % (p.P + 1));
+    const uint32_t row_id = blockIdx.x / uint32_t(p.segs);
+    const int seg = int(blockIdx.x - row_id * uint32_t(p.segs));
+    const int b = int(row_id / uint32_t(p.P + 1)), i = int(row_id - uint32_t(b) * uint32_t(p.P + 1));
     const int n = p.len[b];
     if (i > n || n > p.P) return;                       // a row no proposal is tested in
     const T *row = static_cast<const T *>(p.logits) + b * p.lb + i * p.lp;
@@ -165,41 +199,51 @@ __global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const __grid_con
     const float c = inv_t * 1.4426950408889634f;
     const int mis = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));   // logits before the row in piece 0
     const int pieces = (p.V + mis + E - 1) / E;
-    const int lo = int(int64_t(pieces) * seg / p.segs), hi = int(int64_t(pieces) * (seg + 1) / p.segs);
+    const int per = int((uint32_t(pieces) + uint32_t(p.segs) - 1) / uint32_t(p.segs));
+    const int lo = min(seg * per, pieces), hi = min(lo + per, pieces);
+    const int whole0 = mis ? 1 : 0, whole1 = (p.V + mis) / E;         // pieces [whole0, whole1) are all the row's
     const uint4 *base = reinterpret_cast<const uint4 *>(row - mis);
     const uint32_t none = std::is_same<T, float>::value ? 0xff800000u
                           : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
 
-    auto load = [&](int k) -> uint4 {
-        if (k >= hi) return make_uint4(none, none, none, none);
-        if (k * E >= mis && (k + 1) * E - mis <= p.V) return __ldcs(base + k);
-        union {                                          // a piece that is part of the row only
-            uint4 v;
-            T x[E];
-        } u;
-        u.v = make_uint4(none, none, none, none);
-        for (int e = 0; e < E; ++e) {
-            const int j = k * E + e - mis;
-            if (j >= 0 && j < p.V) u.x[e] = row[j];
-        }
-        return u.v;
-    };
-
     Stat v{-INFINITY, 0.0f, INT32_MAX};
-    uint4 next[kUnroll];
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) next[k] = load(lo + int(threadIdx.x) + k * kStatThreads);
     for (int k0 = lo + int(threadIdx.x); k0 < hi; k0 += kUnroll * kStatThreads) {
-        float x[kUnroll][E];
+        uint4 r[kUnroll];
+        if (k0 >= whole0 && k0 + (kUnroll - 1) * kStatThreads < min(hi, whole1)) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) unpack(next[k], x[k], T());
+            for (int k = 0; k < kUnroll; ++k) r[k] = __ldcs(base + k0 + k * kStatThreads);
+        } else {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) next[k] = load(k0 + (kUnroll + k) * kStatThreads);
-        float big = -INFINITY;                           // (a NaN loses to any number)
+            for (int k = 0; k < kUnroll; ++k) {
+                const int at = k0 + k * kStatThreads;
+                r[k] = make_uint4(none, none, none, none);
+                if (at < hi && at >= whole0 && at < whole1) {
+                    r[k] = __ldcs(base + at);
+                } else if (at < hi) {                    // a piece that is part of the row only
+                    uint32_t w[4] = {none, none, none, none};
+                    for (int e = 0; e < E; ++e) {
+                        const int j = at * E + e - mis;
+                        if (j < 0 || j >= p.V) continue;
+                        if (sizeof(T) == 4) {
+                            w[e % 4] = reinterpret_cast<const uint32_t *>(row)[j];
+                        } else {
+                            const uint32_t x = reinterpret_cast<const uint16_t *>(row)[j];
+                            w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (x << 16) : (w[e / 2] & 0xffff0000u) | x;
+                        }
+                    }
+                    r[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        uint4 top = r[0];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
+        for (int k = 1; k < kUnroll; ++k) top = max_words(top, r[k], T());
+        float big = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < E; ++e) big = fmaxf(big, x[k][e]);
+        for (int w = 0; w < E / 2; ++w) {
+            const float2 x = two(top, w, T());
+            big = fmaxf(big, fmaxf(x.x, x.y));
+        }
         if (big > v.m) {
             v.s = v.m == -INFINITY ? 0.0f : v.s * weight(v.m, big, inv_t);
             v.m = big;
@@ -207,33 +251,46 @@ __global__ void __launch_bounds__(kStatThreads, 3) stats_kernel(const __grid_con
 #pragma unroll
                 for (int k = kUnroll - 1; k >= 0; --k)
 #pragma unroll
-                    for (int e = E - 1; e >= 0; --e)
-                        if (x[k][e] == big) v.at = (k0 + k * kStatThreads) * E + e - mis;
+                    for (int w = E / 2 - 1; w >= 0; --w) {
+                        const float2 x = two(r[k], w, T());
+                        const int j = (k0 + k * kStatThreads) * E + 2 * w - mis;
+                        if (x.y == big) v.at = j + 1;
+                        if (x.x == big) v.at = j;
+                    }
             }
         }
-        float s[4] = {};
+        float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+        const float2 minus_m = make_float2(-v.m, -v.m), cc = make_float2(c, c);
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k)
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[e & 3] += exp2_approx((x[k][e] - v.m) * c);
-        float sum = (s[0] + s[1]) + (s[2] + s[3]);
+            for (int w = 0; w < E / 2; ++w) {
+                const float2 a = mul2(add2(two(r[k], w, T()), minus_m), cc);
+                const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+                if (w & 1) s1 = add2(s1, e);
+                else s0 = add2(s0, e);
+            }
+        float sum = (s0.x + s0.y) + (s1.x + s1.y);
         if (!(sum <= FLT_MAX)) {                         // infinities or NaN among them: one by one
             sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < kUnroll; ++k)
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (x[k][e] > -INFINITY) sum += weight(x[k][e], v.m, inv_t);
+                for (int w = 0; w < E / 2; ++w) {
+                    const float2 x = two(r[k], w, T());
+                    if (x.x > -INFINITY) sum += weight(x.x, v.m, inv_t);
+                    if (x.y > -INFINITY) sum += weight(x.y, v.m, inv_t);
+                }
         }
         v.s += sum;
     }
-    v = warp_join(v, inv_t);
+    v = warp_join(v, inv_t, greedy);
     if ((threadIdx.x & 31) == 0) warp_stat[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
         v = threadIdx.x < kStatThreads / 32 ? warp_stat[threadIdx.x] : Stat{-INFINITY, 0.0f, INT32_MAX};
-        v = warp_join(v, inv_t);
-        if (threadIdx.x == 0) p.part[row_id * p.segs + seg] = make_float4(v.m, v.s, __int_as_float(v.at), 0.0f);
+        v = warp_join(v, inv_t, greedy);
+        if (threadIdx.x == 0) p.part[int64_t(row_id) * p.segs + seg] = make_float4(v.m, v.s, __int_as_float(v.at), 0.0f);
     }
 }
 
@@ -245,7 +302,7 @@ __device__ inline Stat row_stat(const Params &p, int b, int i, float inv_t, int 
         const float4 q = part[k];
         v = join(v, Stat{q.x, q.y, __float_as_int(q.z)}, inv_t);
     }
-    return warp_join(v, inv_t);
+    return warp_join(v, inv_t, true);
 }
 
 // The best race key so far: the largest, at its lowest index.
@@ -277,16 +334,32 @@ __device__ inline uint32_t cluster_rank() {
 }
 __device__ inline void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ inline void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Writes 8 bytes to the same shared-memory place of the cluster's CTA 0.
-__device__ inline void store_to_first(void *place, uint64_t v) {
+// Writes 8 bytes to the same shared-memory place of the cluster's CTA `rank`.
+__device__ inline void store_to(uint32_t rank, void *place, uint64_t v) {
     uint32_t at;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(lkd::smem_addr(place)));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(lkd::smem_addr(place)), "r"(rank));
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
-__device__ inline uint64_t pack(const Best &b) {
-    return (uint64_t(__float_as_uint(b.key)) << 32) | uint32_t(b.at);
+
+// The best of the whole cluster, in every thread of it.  `place` is written by every
+// CTA of the cluster and used once per launch.
+__device__ inline Best cluster_best(Best v, uint64_t (&warps)[kPickThreads / 32], uint64_t (&place)[kMaxCluster],
+                                    int rank, int cluster) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto pack = [](const Best &b) { return (uint64_t(__float_as_uint(b.key)) << 32) | uint32_t(b.at); };
+    auto unpack = [](uint64_t w) { return Best{__uint_as_float(uint32_t(w >> 32)), int32_t(uint32_t(w))}; };
+    v = warp_better(v);
+    if (lane == 0) warps[warp] = pack(v);
+    __syncthreads();
+    if (warp == 0) {
+        v = warp_better(lane < kPickThreads / 32 ? unpack(warps[lane]) : Best{0.0f, INT32_MAX});
+        if (lane < cluster) store_to(lane, &place[rank], pack(v));
+        __syncwarp();
+    }
+    cluster_arrive();
+    cluster_wait();
+    return warp_better(lane < cluster ? unpack(place[lane]) : Best{0.0f, INT32_MAX});
 }
-__device__ inline Best unpack(uint64_t v) { return Best{__uint_as_float(uint32_t(v >> 32)), int32_t(uint32_t(v))}; }
 
 // One cluster per request.  Every CTA of it finds the first rejected position a (a
 // warp per position: its segments joined, its proposal tested), then takes an equal
@@ -296,12 +369,17 @@ template <typename T>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ Params p) {
     __shared__ int s_first;
     __shared__ Stat kept[kKept], s_row;
-    __shared__ Best warp_res[kPickThreads / 32], warp_all[kPickThreads / 32];
-    __shared__ uint64_t cta_res[kMaxCluster], cta_all[kMaxCluster];
-    wait_for_prerequisite_grid();
-    allow_dependent_launch();
+    __shared__ uint64_t warps[3][kPickThreads / 32], places[3][kMaxCluster];
     const int b = blockIdx.x / p.cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = int(cluster_rank());
+    const int per = int((uint32_t(p.V) + uint32_t(p.cluster) - 1) / uint32_t(p.cluster));
+    const int lo = min(rank * per, p.V), hi = min(lo + per, p.V);    // this CTA's part of the race
+    // the noise on its way while stats_kernel's last CTAs run: it is the call's input, and
+    // this grid starts after all of stats_kernel's CTAs have waited for what came before
+    if (p.noise)
+        for (int j = lo + 32 * tid; j < hi; j += 32 * kPickThreads) lkd::prefetch_l2(p.noise + int64_t(b) * p.V + j);
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
     const int P = p.P, n = p.len[b];
     int32_t *commit = p.out_commit + int64_t(b) * (P + 1);
     float *lps = p.out_logprobs ? p.out_logprobs + int64_t(b) * (P + 1) : nullptr;
@@ -355,71 +433,66 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     const T *x = rows + a * p.lp;
     int32_t token = row.m > -INFINITY ? row.at : -1;
     if (!greedy) {
-        // the race: the residual's best key, and p's own for a residual of nothing
-        // (keys without the common factor 1 / s where no q is taken off)
-        cluster_arrive();                                // CTA 0 runs before another writes to it
+        cluster_arrive();                                // every CTA runs before another writes to it
         const bool rejected = a < n;
         const bool point = !p.qprobs || (rejected && p.point_mass && p.point_mass[int64_t(b) * P + a] != 0);
         const int32_t d = rejected && point ? block[a] : -1;
         const float *q = rejected && !point ? p.qprobs + b * p.qb + a * p.qp : nullptr;
         const float *noise = p.noise + int64_t(b) * p.V;
-        const int lo = int(int64_t(p.V) * rank / p.cluster), hi = int(int64_t(p.V) * (rank + 1) / p.cluster);
-        const int last = row.m > -INFINITY ? hi : lo;    // an empty row has no race
-        Best res{-1.0f, INT32_MAX}, all{-1.0f, INT32_MAX};
-        for (int j0 = lo + tid; j0 < last; j0 += kRace * kPickThreads) {
-            float xs[kRace], es[kRace], qs[kRace];
+        const float c = inv_t * 1.4426950408889634f, inv_s = 1.0f / row.s;
+        Best best{0.0f, INT32_MAX};
+        // keys without the common factor 1 / s where no q is taken off.  The best of
+        // kRace keys first; which one it was only where it beats the thread's best.
+        auto race = [&](auto kind) {
+            constexpr bool with_q = decltype(kind)::value;
+            for (int j0 = lo + tid; j0 < hi; j0 += kRace * kPickThreads) {
+                float key[kRace], es[kRace], qs[kRace];
 #pragma unroll
-            for (int k = 0; k < kRace; ++k) {
-                const int j = j0 + k * kPickThreads;
-                const bool in = j < last;
-                xs[k] = in ? logit(x, j) : -INFINITY;
-                es[k] = in ? __ldcs(noise + j) : 1.0f;
-                qs[k] = q && in ? __ldcs(q + j) : 0.0f;
-            }
+                for (int k = 0; k < kRace; ++k) {
+                    const int j = min(j0 + k * kPickThreads, hi - 1);        // past the end: the last one again
+                    key[k] = to_f32(x[j]);
+                    es[k] = __ldcs(noise + j);
+                    if (with_q) qs[k] = __ldcs(q + j);
+                }
+                float top = 0.0f;                        // NaN drops out
 #pragma unroll
-            for (int k = 0; k < kRace; ++k) {
-                const int j = j0 + k * kPickThreads;
-                const float w = weight(xs[k], row.m, inv_t);
-                if (q) {
-                    const float pj = w / row.s, left = pj - qs[k];
-                    if (left > 0.0f) res = better(res, Best{left / es[k], j});
-                    if (pj > 0.0f) all = better(all, Best{pj / es[k], j});
-                } else if (w > 0.0f) {
-                    const Best one{w / es[k], j};
-                    if (j != d) res = better(res, one);
-                    else all = one;                      // the refused token, should nothing else be left
+                for (int k = 0; k < kRace; ++k) {
+                    const float w = exp2_approx((key[k] - row.m) * c);
+                    key[k] = __fdividef(with_q ? fmaf(w, inv_s, -qs[k]) : w, es[k]);
+                    top = fmaxf(top, key[k]);
+                }
+                if (top > best.key) {
+#pragma unroll
+                    for (int k = 0; k < kRace; ++k) {
+                        const int j = min(j0 + k * kPickThreads, hi - 1);
+                        if (key[k] > best.key && j != d) best = Best{key[k], j};
+                    }
                 }
             }
+        };
+        const bool plain = row.m > -INFINITY && row.m <= FLT_MAX && c <= FLT_MAX;
+        if (plain) {
+            if (q) race(std::true_type());
+            else race(std::false_type());
         }
-        res = warp_better(res);
-        all = warp_better(all);
-        if (lane == 0) {
-            warp_res[warp] = res;
-            warp_all[warp] = all;
-        }
-        __syncthreads();
         cluster_wait();
-        if (warp == 0) {
-            res = lane < kPickThreads / 32 ? warp_res[lane] : Best{-1.0f, INT32_MAX};
-            all = lane < kPickThreads / 32 ? warp_all[lane] : Best{-1.0f, INT32_MAX};
-            res = warp_better(res);
-            all = warp_better(all);
-            if (lane == 0) {
-                store_to_first(&cta_res[rank], pack(res));
-                store_to_first(&cta_all[rank], pack(all));
+        best = cluster_best(best, warps[0], places[0], rank, p.cluster);
+        if (best.key == 0.0f && row.m > -INFINITY) {
+            // nothing left above 2^-126, or infinite logits: once more, to the smallest
+            // float32, with p's own best should the residual be nothing at all
+            Best all{0.0f, INT32_MAX};
+            for (int j = lo + tid; j < hi; j += kPickThreads) {
+                const float w = weight(logit(x, j), row.m, inv_t), own = w / noise[j];
+                const float key = q ? (w / row.s - q[j]) / noise[j] : own;
+                if (key > best.key && j != d) best = Best{key, j};
+                if (own > all.key) all = Best{own, j};
             }
+            best = cluster_best(best, warps[1], places[1], rank, p.cluster);
+            all = cluster_best(all, warps[2], places[2], rank, p.cluster);
+            if (best.key == 0.0f) best = all;
         }
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
         if (rank) return;
-        if (warp == 0) {
-            res = lane < p.cluster ? unpack(cta_res[lane]) : Best{-1.0f, INT32_MAX};
-            all = lane < p.cluster ? unpack(cta_all[lane]) : Best{-1.0f, INT32_MAX};
-            res = warp_better(res);
-            all = warp_better(all);
-            token = res.key >= 0.0f ? res.at : (all.key >= 0.0f ? all.at : -1);
-        }
+        token = best.key > 0.0f ? best.at : -1;
     }
     if (warp == 0) {
         for (int i = lane; i <= P; i += 32) {
@@ -440,21 +513,22 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     }
 }
 
-// Segments of a row: enough CTAs for two waves of stats_kernel where rows are few,
-// at most kSegMax logits each and, where that leaves a choice, at least kSegMin.
-int segments(int32_t B, int32_t P, int32_t V) {
+// Segments of a row of `size`-byte logits: enough CTAs for two waves of stats_kernel
+// where rows are few, at most kSegBytes each.
+int segments(int32_t B, int32_t P, int32_t V, int size) {
     const int64_t rows = int64_t(B) * (P + 1);
     const int64_t want = 152 * 8 / (rows > 0 ? rows : 1) + 1;
-    const int64_t least = (int64_t(V) + kSegMax - 1) / kSegMax, most = (int64_t(V) + kSegMin - 1) / kSegMin;
+    const int64_t least = (int64_t(V) * size + kSegBytes - 1) / kSegBytes, most = (int64_t(V) + kSegMin - 1) / kSegMin;
     int64_t s = want < most ? want : most;
     s = s > least ? s : least;
     return int(s > kMaxSegs ? kMaxSegs : s);
 }
 
-// CTAs of a request's cluster: one per 16384 logits of its race, a power of two.
-int cluster_for(int32_t V) {
+// CTAs of a request's cluster: a power of two, one per 4096 logits of its race as
+// long as all clusters run at once (two CTAs per SM).
+int cluster_for(int32_t B, int32_t V) {
     int c = 1;
-    while (c < kMaxCluster && int64_t(c) * 16384 < V) c *= 2;
+    while (c < kMaxCluster && int64_t(c) * 4096 < V && int64_t(2) * c * B <= 304) c *= 2;
     return c;
 }
 
@@ -488,7 +562,7 @@ extern "C" {
 
 size_t lookup_verify_logits_workspace_bytes(int32_t B, int32_t P, int32_t V) {
     if (B < 0 || P < 0 || P > kMaxBlock || V < 1 || V >= kMaxV) return 0;
-    return size_t(B) * size_t(P + 1) * size_t(segments(B, P, V)) * sizeof(float4) + 16;
+    return size_t(B) * size_t(P + 1) * size_t(segments(B, P, V, 4)) * sizeof(float4) + 16;
 }
 
 int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *logits, const int64_t *logits_strides,
@@ -500,7 +574,7 @@ int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *l
     if (B < 0 || P < 0 || P > kMaxBlock || V < 1 || V >= kMaxV) return LOOKUP_DRAFT_EINVAL;
     if (type != LOOKUP_TYPE_F32 && type != LOOKUP_TYPE_F16 && type != LOOKUP_TYPE_BF16) return LOOKUP_DRAFT_EINVAL;
     if (B == 0) return LOOKUP_DRAFT_OK;
-    const int segs = segments(B, P, V);
+    const int segs = segments(B, P, V, type == LOOKUP_TYPE_F32 ? 4 : 2);
     if (int64_t(B) * (P + 1) * segs > INT32_MAX || int64_t(B) * kMaxCluster > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
     if ((P > 0 && !block) || !len || !logits || !logits_strides || !out_accepted || !out_commit || !out_ncommit ||
         !workspace)
@@ -518,7 +592,7 @@ int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *l
     const bool with_q = noise && qprobs && P > 0;
     Params p{block, len, logits, logits_strides[0], logits_strides[1], noise, noise ? temperature : nullptr, u,
              with_q ? qprobs : nullptr, with_q ? qprobs_strides[0] : 0, with_q ? qprobs_strides[1] : 0, point_mass,
-             B, P, V, segs, cluster_for(V), out_accepted, out_commit, out_ncommit, out_logprobs, static_cast<float4 *>(workspace)};
+             B, P, V, segs, cluster_for(B, V), out_accepted, out_commit, out_ncommit, out_logprobs, static_cast<float4 *>(workspace)};
     if (type == LOOKUP_TYPE_F32) return launch<float>(p, stream);
     if (type == LOOKUP_TYPE_F16) return launch<__half>(p, stream);
     return launch<__nv_bfloat16>(p, stream);
