@@ -33,6 +33,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -51,11 +52,12 @@ constexpr int kTile = 64;                // positions of a tile
 constexpr int kSoftWarps = 4;            // one thread per row
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kThreads = 192;
-constexpr int kJoinRows = 8;             // rows a CTA of join_kernel finishes
-constexpr int kJoinThreads = 32 * kJoinRows;
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;       // of a CTA of join_kernel
+constexpr int kJoinRows = 4;             // rows it joins at a time where an item has many parts
+constexpr int kFewParts = 4;             // parts that a warp joins by itself
 constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
 constexpr int kMaxCtas = 2 * kMaxSms;
-constexpr int kItemUnits = 3;            // what an item's begin and end cost, in tiles
+constexpr int kItemUnits = 8;            // what an item's begin and end cost, in tiles
 constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
 constexpr int kBarBytes = 1024;          // barriers and small state ahead of the tiles
 
@@ -269,6 +271,10 @@ __device__ inline void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ inline void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ inline float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -291,7 +297,7 @@ __device__ inline uint32_t pack2(float lo, float hi, __nv_bfloat16) {
 // Ahead of the tiles: barriers (8 bytes each) and a few words.
 struct Head {
     uint64_t full[16], empty[16];        // slots
-    uint64_t s_full[2], p_ready[2], pv_done[2], q_ready, drain;
+    uint64_t s_full[2], p_ready[2], pv_done[2], q_ready, staged, drain;
     uint32_t tmem, failed;
     int32_t start_r;
     int64_t start_off, total;
@@ -346,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             mbar_init(smem_addr(&hd.pv_done[k]), 1);
         }
         mbar_init(smem_addr(&hd.q_ready), kRows);
+        mbar_init(smem_addr(&hd.staged), kRows);
         mbar_init(smem_addr(&hd.drain), 1);
         lkd::fence_barrier_init();
         hd.failed = 0;
@@ -512,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         // ---- softmax: a thread per row ----
         const uint32_t lanes = uint32_t(warp * 32) << 16;
         const int row = warp * 32 + lane;
-        uint32_t it = 0;
+        uint32_t it = 0, item = 0;
+        unsigned char *stage = smem + kBarBytes + warp * 4096;       // 32 rows of 128 bytes, in Q's place
         Meta meta{-1, 0, 0, 0, 0, 0, 0, 0};
         bool ok = true;
         // rows of the block past q_len, and those of requests that see nothing
@@ -524,32 +532,36 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             if (p.lse)
                 for (int64_t x = i0 + row; x < i1; x += kRows) p.lse[x] = -INFINITY;
         }
-        for (; count > 0 && ok && wk.valid(); wk.next(p)) {
+        for (; count > 0 && ok && wk.valid(); wk.next(p), ++item) {
             const Request &q = wk.q;
             const int rows = min(kRows, q.n * p.G - wk.mt * kRows);
             const int rr = wk.mt * kRows + row;          // row of the request: token, then head of the group
             const bool live = row < rows;
             const int i = live ? rr / p.G : 0;
             const int head = wk.h * p.G + (live ? rr - i * p.G : 0);
-            // Q, 16 bytes at a time, where the products' swizzle wants it (idle rows keep what
-            // was there: a row of S depends on its own row of Q only)
+            // Q, 16 bytes at a time, where the products' swizzle wants it, all copies in
+            // flight together (idle rows keep what was there: a row of S depends on its own
+            // row of Q only).  Before it, the last item's result has left these bytes.
+            if (item > 0 && !warp_wait(smem_addr(&hd.staged), (item - 1) & 1, failed, p.limit_ns)) {
+                ok = false;
+                break;
+            }
             {
                 constexpr int kCh = D / 8, kStep = kRows / kCh;          // chunks of a row, rows of a pass
                 const int ch = row % kCh;
                 const T *src = static_cast<const T *>(p.q) + wk.r * p.qb + wk.h * p.G * p.qh + ch * 8;
                 unsigned char *dst = smem + kBarBytes + (ch >> 3) * (kRows * 128);
-#pragma unroll 4
                 for (int y = row / kCh; y < rows; y += kStep) {
                     const uint32_t ry = wk.mt * kRows + y, iy = ry / uint32_t(p.G);
-                    uint4 v = *reinterpret_cast<const uint4 *>(src + iy * p.qn + (ry - iy * p.G) * p.qh);
-                    if (p.negate) {
-                        v.x ^= 0x80008000u;
-                        v.y ^= 0x80008000u;
-                        v.z ^= 0x80008000u;
-                        v.w ^= 0x80008000u;
-                    }
-                    *reinterpret_cast<uint4 *>(dst + y * 128 + (((ch & 7) ^ (y & 7)) << 4)) = v;
+                    copy16(smem_addr(dst + y * 128 + (((ch & 7) ^ (y & 7)) << 4)),
+                           src + iy * p.qn + (ry - iy * p.G) * p.qh);
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                if (p.negate)
+                    for (int y = row / kCh; y < rows; y += kStep) {
+                        uint4 *v = reinterpret_cast<uint4 *>(dst + y * 128 + (((ch & 7) ^ (y & 7)) << 4));
+                        *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
+                    }
                 lkd::fence_proxy_async_smem();
                 mbar_arrive(smem_addr(&hd.q_ready));
             }
@@ -664,34 +676,50 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                 break;
             }
             tc_fence_after();
-            // the item's end: its rows, or this CTA's part of them
+            // the item's end: its rows, or this CTA's part of them.  Each thread has a row; 128
+            // bytes of every row of the warp at a time go through shared memory (16-byte
+            // pieces swizzled by the row), so that whole lines are written.
             const bool whole = wk.a == 0 && wk.b == q.nt;
+            const int my_row = lane >> 3, my_piece = lane & 7;       // of four rows at a time
             if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const int64_t o_row = (int64_t(wk.r) * p.N + i) * p.Hq + head;
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + o_row * D);
                 if (warp_live) {
 #pragma unroll
-                    for (int j = 0; j < D; j += 32) {
-                        uint32_t o[32];
-                        tc_ld32(tmem + lanes + S::kO + j, o);
-                        tc_wait_ld(o);
-                        if (live) {
+                    for (int j = 0; j < D; j += 64) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8) {
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t o[32];
+                            tc_ld32(tmem + lanes + S::kO + j + 32 * half, o);
+                            tc_wait_ld(o);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
                                 uint32_t w[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float lo = __uint_as_float(o[k + 2 * e]) * inv;
-                                    const float hi = __uint_as_float(o[k + 2 * e + 1]) * inv;
-                                    w[e] = sum == 0.0f ? 0u : pack2(lo, hi, T());   // a row that sees nothing
-                                }
-                                dst[(j + k) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                                for (int e = 0; e < 4; ++e)          // (a row that sees nothing is 0)
+                                    w[e] = sum == 0.0f ? 0u
+                                                       : pack2(__uint_as_float(o[8 * k + 2 * e]) * inv,
+                                                               __uint_as_float(o[8 * k + 2 * e + 1]) * inv, T());
+                                *reinterpret_cast<uint4 *>(stage + lane * 128 + (((4 * half + k) ^ (lane & 7)) << 4)) =
+                                    make_uint4(w[0], w[1], w[2], w[3]);
                             }
                         }
+                        __syncwarp();
+#pragma unroll
+                        for (int t = 0; t < 32; t += 4) {
+                            const int y = t + my_row;
+                            if (warp * 32 + y < rows) {
+                                const uint32_t ry = wk.mt * kRows + warp * 32 + y, iy = ry / uint32_t(p.G);
+                                const int64_t o_row =
+                                    (int64_t(wk.r) * p.N + iy) * p.Hq + wk.h * p.G + (ry - iy * uint32_t(p.G));
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + o_row * D + j + my_piece * 8) =
+                                    *reinterpret_cast<const uint4 *>(stage + y * 128 + ((my_piece ^ (y & 7)) << 4));
+                            }
+                        }
+                        __syncwarp();
                     }
                     if (live && p.lse)
-                        p.lse[o_row] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (m * p.c + log2f(sum));
+                        p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
+                            sum == 0.0f ? -INFINITY : 0.6931471805599453f * (m * p.c + log2f(sum));
                 }
             } else {
                 // slot 2c + 1: the item began here; 2c: it began in an earlier range
@@ -703,12 +731,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         uint32_t o[32];
                         tc_ld32(tmem + lanes + S::kO + j, o);
                         tc_wait_ld(o);
-                        if (live) {
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                *reinterpret_cast<uint4 *>(ws + row * D + j + k) =
-                                    make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int t = 0; t < 32; t += 4) {
+                            const int y = t + my_row;
+                            if (warp * 32 + y < rows)
+                                *reinterpret_cast<uint4 *>(ws + (warp * 32 + y) * D + j + my_piece * 4) =
+                                    *reinterpret_cast<const uint4 *>(stage + y * 128 + ((my_piece ^ (y & 7)) << 4));
                         }
+                        __syncwarp();
                     }
                     if (live) {
                         ws[D * p.part_rows + row] = m;
@@ -725,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                 }
             }
             tc_fence_before();                           // O is read before the next item's products (p_ready)
+            mbar_arrive(smem_addr(&hd.staged));
         }
         if (row == 0) {
             meta.failed = ok ? 0 : 1;
@@ -740,16 +776,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
 }
 
 // Joins the parts of the item that CTA blockIdx.x of attention_kernel began and did
-// not end, a warp per row: the weights 2^(c (m_k - M)) of the row's parts, a lane per
-// part, then the sum of the parts, a lane per D / 32 columns, its loads independent
-// of each other.  A wait that ran out anywhere makes the whole call's rows NaN.
+// not end.  Few parts (many items, each cut once or twice): a warp per row, the parts'
+// maxima, sums and rows loaded together.  Many (few long items): kJoinRows rows at a
+// time, first their weights 2^(c (m_k - M)), a warp per row and a lane per part; then
+// each warp sums every eighth part over those rows, and the warps' sums are added.  A wait that ran out anywhere makes the whole call's rows NaN.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 4) join_kernel(const __grid_constant__ Params p) {
     constexpr int E = D / 32;                            // columns of a lane
-    __shared__ float weights[kJoinRows][kMaxCtas];
+    __shared__ float weights[kJoinRows][kMaxCtas], s_big[kJoinRows], s_sum[kJoinRows];
+    __shared__ float sums[kJoinWarps][kJoinRows][D];
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
     const Meta meta = p.meta[c];
     int bad = 0;
     for (int k = tid; k < p.ctas; k += kJoinThreads) bad |= p.meta[k].failed;
@@ -762,50 +800,118 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             for (int64_t x = first; x < rows; x += step) p.lse[x] = NAN;
         return;
     }
-    const int row = blockIdx.y * kJoinRows + (tid >> 5);
-    if (meta.r < 0 || row >= meta.rows) return;
+    if (meta.r < 0) return;
     const int64_t size = int64_t(D + 2) * p.part_rows;   // of a part
     const int count = meta.last - c + 1;
     const float *own = p.parts + int64_t(2 * c + 1) * size, *more = own + size;    // the first, then every second
     auto part = [&](int k) { return k ? more + int64_t(2 * (k - 1)) * size : own; };
-    float *weight = weights[tid >> 5];
-    float big = -INFINITY, sum = 0.0f;
-    for (int k = lane; k < count; k += 32) {
-        const float mk = part(k)[D * p.part_rows + row], sk = part(k)[(D + 1) * p.part_rows + row];
-        weight[k] = sk == 0.0f ? -INFINITY : mk;         // a part the row sees nothing of
-        if (sk != 0.0f) big = fmaxf(big, mk);
-    }
+    auto place = [&](int row) {                          // the row's place in out / D and in lse
+        const int rr = meta.mt * kRows + row, i = rr / p.G;
+        return (int64_t(meta.r) * p.N + i) * p.Hq + meta.h * p.G + (rr - i * p.G);
+    };
+    auto finish = [&](int row, const float (&o)[E], float big, float sum) {          // a warp's row
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + place(row) * D + lane * E);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-    for (int k = lane; k < count; k += 32) {
-        const float mk = weight[k];
-        const float w = mk == -INFINITY ? 0.0f : exp2f((mk - big) * p.c);
-        weight[k] = w;
-        if (w != 0.0f) sum += w * part(k)[(D + 1) * p.part_rows + row];
-    }
+        for (int e = 0; e < E / 2; ++e) dst[e] = sum == 0.0f ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv, T());
+        if (lane == 0 && p.lse)
+            p.lse[place(row)] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(sum));
+    };
+    if (count <= kFewParts) {
+        // a warp per row, the parts' maxima, sums and rows loaded together
+        for (int row = blockIdx.y * kJoinWarps + warp; row < meta.rows; row += gridDim.y * kJoinWarps) {
+            float m[kFewParts], s[kFewParts], o[E] = {};
+            float2 v[kFewParts][E / 2];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    __syncwarp();
-    float o[E] = {};
-#pragma unroll 8
-    for (int k = 0; k < count; ++k) {
-        const float w = weight[k];
-        const float2 *src = reinterpret_cast<const float2 *>(part(k) + row * D + lane * E);
+            for (int k = 0; k < kFewParts; ++k) {
+                const float *src = part(k < count ? k : 0);
+                m[k] = k < count ? src[D * p.part_rows + row] : -INFINITY;
+                s[k] = k < count ? src[(D + 1) * p.part_rows + row] : 0.0f;      // 0: the row sees nothing of the part
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-            const float2 v = src[e];
-            o[2 * e] += w == 0.0f ? 0.0f : w * v.x;
-            o[2 * e + 1] += w == 0.0f ? 0.0f : w * v.y;
+                for (int e = 0; e < E / 2; ++e)
+                    v[k][e] = reinterpret_cast<const float2 *>(src + row * D + lane * E)[e];
+            }
+            float big = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kFewParts; ++k)
+                if (s[k] != 0.0f) big = fmaxf(big, m[k]);
+#pragma unroll
+            for (int k = 0; k < kFewParts; ++k) {
+                const float w = s[k] == 0.0f ? 0.0f : m[k] == big ? 1.0f : exp2f((m[k] - big) * p.c);
+                if (w == 0.0f) continue;
+                sum += w * s[k];
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    o[2 * e] += w * v[k][e].x;
+                    o[2 * e + 1] += w * v[k][e].y;
+                }
+            }
+            finish(row, o, big, sum);
         }
+        return;
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = meta.mt * kRows + row, i = rr / p.G;
-    const int64_t o_row = (int64_t(meta.r) * p.N + i) * p.Hq + meta.h * p.G + (rr - i * p.G);
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + o_row * D + lane * E);
+    for (int row0 = blockIdx.y * kJoinRows; row0 < meta.rows; row0 += gridDim.y * kJoinRows) {
+        const int rows = min(kJoinRows, meta.rows - row0);
+        if (warp < rows) {
+            const int row = row0 + warp;
+            float *weight = weights[warp];
+            float big = -INFINITY, sum = 0.0f;
+            for (int k = lane; k < count; k += 32) {
+                const float mk = part(k)[D * p.part_rows + row], sk = part(k)[(D + 1) * p.part_rows + row];
+                weight[k] = sk == 0.0f ? -INFINITY : mk;
+                if (sk != 0.0f) big = fmaxf(big, mk);
+            }
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) dst[e] = sum == 0.0f ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv, T());
-    if (lane == 0 && p.lse)
-        p.lse[o_row] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(sum));
+            for (int d = 16; d; d >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+            for (int k = lane; k < count; k += 32) {
+                const float mk = weight[k];
+                const float w = mk == -INFINITY ? 0.0f : exp2f((mk - big) * p.c);
+                weight[k] = w;
+                if (w != 0.0f) sum += w * part(k)[(D + 1) * p.part_rows + row];
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0) {
+                s_big[warp] = big;
+                s_sum[warp] = sum;
+            }
+        }
+        __syncthreads();
+        float o[kJoinRows][E] = {};
+#pragma unroll 2
+        for (int k = warp; k < count; k += kJoinWarps) {
+            const float2 *src = reinterpret_cast<const float2 *>(part(k) + row0 * D + lane * E);
+            float2 v[kJoinRows][E / 2];
+#pragma unroll
+            for (int y = 0; y < kJoinRows; ++y)
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) v[y][e] = y < rows ? src[y * (D / 2) + e] : make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int y = 0; y < kJoinRows; ++y) {
+                const float w = y < rows ? weights[y][k] : 0.0f;
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) {
+                    o[y][2 * e] += w == 0.0f ? 0.0f : w * v[y][e].x;
+                    o[y][2 * e + 1] += w == 0.0f ? 0.0f : w * v[y][e].y;
+                }
+            }
+        }
+        // the warps' sums; then warp y adds and finishes row y
+#pragma unroll
+        for (int y = 0; y < kJoinRows; ++y)
+#pragma unroll
+            for (int e = 0; e < E; ++e) sums[warp][y][e * 32 + lane] = o[y][e];
+        __syncthreads();
+        if (warp < rows) {
+            float all[E] = {};
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w)
+#pragma unroll
+                for (int e = 0; e < E; ++e) all[e] += sums[w][warp][e * 32 + lane];
+            finish(row0 + warp, all, s_big[warp], s_sum[warp]);
+        }
+        __syncthreads();                                 // shared memory has been read
+    }
 }
 
 // -------------------------------------------------------------------- host ----
@@ -873,7 +979,11 @@ int launch(Params &p, cudaStream_t stream) {
     cudaError_t r = cudaLaunchKernelEx(&cfg, attention_kernel<T, D>, p);
     if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
     lookup_note_launch();
-    cfg.gridDim = dim3(p.ctas, (p.part_rows + kJoinRows - 1) / kJoinRows);
+    // CTAs per item in the join: with about as many items as CTAs each is cut once or
+    // twice and a few CTAs do; a few long items have tens of parts and take them all
+    const int64_t items = int64_t(p.B) * p.Hkv * ((int64_t(p.N) * p.G + kRows - 1) / kRows);
+    const int most = (p.part_rows + kJoinRows - 1) / kJoinRows;
+    cfg.gridDim = dim3(p.ctas, 3 * items >= p.ctas ? std::min(most, 4) : std::min(most, 16));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     r = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p);
