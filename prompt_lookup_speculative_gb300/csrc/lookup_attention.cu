@@ -16,6 +16,13 @@
 // rows by 64 positions into tensor memory, softmax by one thread per row, P back
 // into tensor memory over S, O += P V from there.
 //
+// Few rows: the tile has idle rows, and only the warps of the live ones have a softmax
+// to do, one SM quarter per 32 rows.  So a block of at most 64 (32) rows is in the tile
+// two (four) times, and each copy's threads take a half (a quarter) of the columns:
+// every quarter of the SM works, and a tile's softmax takes a half (a quarter) of the
+// time.  The product of 16 positions goes into their copy's lanes only, and the
+// copies' sums are added at the end.
+//
 // Split: the work of all requests, heads and row tiles is laid end to end in units
 // of 64 positions and cut into equal contiguous ranges, one per CTA (two CTAs per
 // SM), so that neither ragged lengths nor few requests leave an SM without work.
@@ -48,7 +55,6 @@ using lkd::smem_addr;
 using lkd::wait_for_prerequisite_grid;
 
 constexpr int kRows = 128;               // rows of a tile: M of the products, lanes of tensor memory
-constexpr int kTile = 64;                // positions of a tile
 constexpr int kSoftWarps = 4;            // one thread per row
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kThreads = 192;
@@ -56,21 +62,33 @@ constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;       // of a CTA 
 constexpr int kJoinRows = 4;             // rows it joins at a time where an item has many parts
 constexpr int kFewParts = 4;             // parts that a warp joins by itself
 constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
-constexpr int kMaxCtas = 2 * kMaxSms;
-constexpr int kItemUnits = 8;            // what an item's begin and end cost, in tiles
 constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
 constexpr int kBarBytes = 1024;          // barriers and small state ahead of the tiles
 
-// Shared memory and tensor memory of head size D.  A slot holds one tile of K or V.
+// Shared memory and tensor memory of head size D.  A slot holds one tile of K, of V or of both.
 template <int D>
 struct Shape {
     static constexpr int kCtas = D == 256 ? 1 : 2;           // per SM
-    static constexpr int kSlotBytes = kTile * D * 2;
+    // Positions of a tile.  The thread that issues the products takes 0.8 us a tile (four
+    // waits, a dozen instructions of 40 ns); at D = 64 a tile of 64 positions has 16 KB,
+    // for which that is too long (94 us where tiles of 128 take 7x us, ragged lengths).
+    static constexpr int kTile = D == 64 ? 128 : 64;
+    static constexpr int kItemUnits = D == 64 ? 4 : 8;       // what an item's begin and end cost, in tiles
+    // D = 64: K and V share a slot (a wait and a commit less), and one S tile is enough,
+    // since P has tensor memory of its own: the next S comes as soon as this one is read.
+    // Otherwise two S tiles, P over S, and slots for K and V apart, which fill earlier.
+    static constexpr bool kPair = D == 64, kOwnP = D == 64;
+    static constexpr int kTileBytes = kTile * D * 2;         // of K or of V
+    static constexpr int kSlotBytes = kPair ? 2 * kTileBytes : kTileBytes;
     static constexpr int kQBytes = kRows * D * 2;
     static constexpr int kSlots = D == 256 ? 5 : (112 * 1024 - kQBytes) / kSlotBytes;
     static constexpr int kSmem = kBarBytes + kQBytes + kSlots * kSlotBytes;
-    static constexpr int kCols = D == 256 ? 512 : 256;       // tensor memory: S twice, O
-    static constexpr int kO = 2 * kTile;                     // O's first column
+    static constexpr int kBufs = kOwnP ? 1 : 2;              // S tiles in flight
+    static constexpr int kCols = D == 256 ? 512 : 256;       // tensor memory: S, P where it is apart, O
+    static constexpr int kP = kOwnP ? kBufs * kTile : 0, kPStep = kOwnP ? kTile / 2 : kTile;
+    static constexpr int kO = kOwnP ? kP + kBufs * kPStep : kBufs * kTile;
+    static_assert(kO + D <= kCols, "tensor memory");
+    static constexpr int kAhead = 1;                         // S products issued before the oldest P V
 };
 
 struct Meta {                            // one per CTA: the item it began and did not end
@@ -90,7 +108,7 @@ struct Params {
     float *lse;
     Meta *meta;                          // [ctas]
     float *parts;                        // [2 * ctas]: O [part_rows][D], m [part_rows], sum [part_rows]
-    uint64_t limit_ns;
+    uint64_t limit;                      // clocks that a wait may take
 };
 
 // ---------------------------------------------------------------- the work ----
@@ -101,6 +119,7 @@ struct Request {
     int32_t t0, nt, mts;                 // first tile, tiles, row tiles
 };
 
+template <typename S>
 __device__ inline Request request_of(const Params &p, int r) {
     Request q;
     q.n = p.q_len ? min(max(p.q_len[r], 0), p.N) : p.N;
@@ -110,8 +129,8 @@ __device__ inline Request request_of(const Params &p, int r) {
     if (q.n == 0 || q.end <= q.lo) {
         q.t0 = q.nt = 0;
     } else {
-        q.t0 = int32_t(q.lo / kTile);
-        q.nt = int32_t((q.end + kTile - 1) / kTile) - q.t0;
+        q.t0 = int32_t(q.lo / S::kTile);
+        q.nt = int32_t((q.end + S::kTile - 1) / S::kTile) - q.t0;
     }
     q.mts = (q.n * p.G + kRows - 1) / kRows;
     return q;
@@ -119,12 +138,17 @@ __device__ inline Request request_of(const Params &p, int r) {
 
 // Units: an item's tiles, after kItemUnits for its begin and end (its Q, its result), so
 // that a CTA with many short items gets fewer tiles.
-__device__ inline int32_t item_units(const Request &q) { return q.nt ? q.nt + kItemUnits : 0; }
+template <typename S>
+__device__ inline int32_t item_units(const Request &q) {
+    return q.nt ? q.nt + S::kItemUnits : 0;
+}
+template <typename S>
 __device__ inline int64_t units_of(const Params &p, const Request &q) {
-    return int64_t(p.Hkv) * q.mts * item_units(q);
+    return int64_t(p.Hkv) * q.mts * item_units<S>(q);
 }
 
 // A CTA's walk over its range of units, item by item; every role takes the same steps.
+template <typename S>
 struct Walk {
     int32_t r, h, mt;
     Request q;
@@ -135,21 +159,21 @@ struct Walk {
     __device__ void start(const Params &p, int32_t r0, int64_t off, int64_t count) {
         r = r0;
         left = count;
-        q = request_of(p, r);
+        q = request_of<S>(p, r);
         a = b = 0;
         if (count <= 0) return;
-        const int64_t item = off / item_units(q);
+        const int64_t item = off / item_units<S>(q);
         h = int32_t(item / q.mts);
         mt = int32_t(item % q.mts);
-        u = int32_t(off - item * item_units(q));
+        u = int32_t(off - item * item_units<S>(q));
         take();
         if (b == 0) next(p);
     }
     __device__ void take() {
-        const int64_t can = item_units(q) - u;
+        const int64_t can = item_units<S>(q) - u;
         const int32_t n = int32_t(left < can ? left : can);
-        a = max(u - kItemUnits, 0);
-        b = max(u + n - kItemUnits, 0);
+        a = max(u - S::kItemUnits, 0);
+        b = max(u + n - S::kItemUnits, 0);
         left -= n;
     }
     __device__ bool valid() const { return b > 0; }
@@ -164,7 +188,7 @@ struct Walk {
                     h = 0;
                     do {                                 // left > 0: a later request has units
                         if (++r >= p.B) return;
-                        q = request_of(p, r);
+                        q = request_of<S>(p, r);
                     } while (q.nt == 0);
                 }
             }
@@ -204,9 +228,20 @@ __device__ inline void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id
         "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
         : "memory");
 }
+// The same into some of the warps' lanes only: bit w of `quads` set = lanes 32 w .. 32 w + 31.
+__device__ inline void tc_mma_ts_quads(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t quads) {
+    const uint32_t off0 = quads & 1 ? 0u : ~0u, off1 = quads & 2 ? 0u : ~0u;
+    const uint32_t off2 = quads & 4 ? 0u : ~0u, off3 = quads & 8 ? 0u : ~0u;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate)), "r"(off0), "r"(off1), "r"(off2), "r"(off3)
+        : "memory");
+}
 
-// 32 columns of this warp's 32 lanes, and the wait that makes them usable.
-__device__ inline void tc_ld32(uint32_t addr, uint32_t (&r)[32]) {
+// 32 or 16 columns of this warp's 32 lanes, and the wait that makes them usable; the
+// stores of 32, 16 or 8.
+__device__ inline void tc_ld(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -225,7 +260,7 @@ __device__ inline void tc_wait_ld(uint32_t (&r)[32]) {
                    "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ inline void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ inline void tc_st(uint32_t addr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -235,6 +270,33 @@ __device__ inline void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
         "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
         : "memory");
+}
+__device__ inline void tc_ld(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ inline void tc_wait_ld(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])::"memory");
+}
+__device__ inline void tc_st(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+        : "memory");
+}
+__device__ inline void tc_st(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr)
+                 : "memory");
 }
 __device__ inline void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -297,7 +359,7 @@ __device__ inline uint32_t pack2(float lo, float hi, __nv_bfloat16) {
 // Ahead of the tiles: barriers (8 bytes each) and a few words.
 struct Head {
     uint64_t full[16], empty[16];        // slots
-    uint64_t s_full[2], p_ready[2], pv_done[2], q_ready, staged, drain;
+    uint64_t s_full[3], p_ready[3], pv_done[3], q_ready, staged, sync, s_free, drain;
     uint32_t tmem, failed;
     int32_t start_r;
     int64_t start_off, total;
@@ -305,33 +367,53 @@ struct Head {
 };
 static_assert(sizeof(Head) <= kBarBytes, "Head fits ahead of the tiles");
 
-// Waits for phase `parity` of the barrier, at most limit_ns and only while no other
-// wait of the CTA has run out; false otherwise.
-__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
-    const uint64_t from = lkd::global_ns();
+__device__ inline bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Waits for phase `parity` of the barrier, at most `limit` clocks and only while no
+// other wait of the CTA has run out; false otherwise.
+__device__ inline bool wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t from = clock64();
     for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
         if (*failed) return false;
-        if (lkd::global_ns() - from > limit_ns) {
+        if (uint64_t(clock64()) - from > limit) {
             *failed = 1;
             return false;
         }
+        if (mbar_try_wait(bar, parity)) return true;
     }
 }
 
-__device__ inline bool wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return slow_wait(bar, parity, failed, limit_ns);
-}
-
 // The same for a whole warp: every lane waits, and all go on or none does.
-__device__ inline bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit_ns) {
-    return __all_sync(0xffffffffu, wait(bar, parity, failed, limit_ns));
+__device__ inline bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit) {
+    return __all_sync(0xffffffffu, wait(bar, parity, failed, limit));
 }
 
-template <typename T, int D>
+// A place in a ring of N and the parity of how often the ring has been round.
+template <int N>
+struct Place {
+    uint32_t at, phase;
+    __device__ void step(uint32_t by) {
+        at += by;
+        if (at >= N) {
+            at -= N;
+            phase ^= 1;
+        }
+    }
+};
+
+template <typename T, int D, int REP>
 __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(const __grid_constant__ Params p) {
     using S = Shape<D>;
+    constexpr int kTile = S::kTile;
     extern __shared__ __align__(1024) unsigned char smem[];
     Head &hd = *reinterpret_cast<Head *>(smem);
     const uint32_t q_smem = smem_addr(smem) + kBarBytes;
@@ -346,13 +428,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < S::kBufs; ++k) {
             mbar_init(smem_addr(&hd.s_full[k]), 1);
             mbar_init(smem_addr(&hd.p_ready[k]), kRows);
             mbar_init(smem_addr(&hd.pv_done[k]), 1);
         }
         mbar_init(smem_addr(&hd.q_ready), kRows);
         mbar_init(smem_addr(&hd.staged), kRows);
+        mbar_init(smem_addr(&hd.sync), kRows);
+        mbar_init(smem_addr(&hd.s_free), kRows);
         mbar_init(smem_addr(&hd.drain), 1);
         lkd::fence_barrier_init();
         hd.failed = 0;
@@ -367,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
     // the range of this CTA: units [start, stop) of all requests' units end to end
     {
         int64_t own = 0;
-        for (int r = tid; r < p.B; r += kThreads) own += units_of(p, request_of(p, r));
+        for (int r = tid; r < p.B; r += kThreads) own += units_of<S>(p, request_of<S>(p, r));
 #pragma unroll
         for (int d = 16; d; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
         if (lane == 0) hd.warp_sum[warp] = own;
@@ -386,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         int64_t before = 0;                              // units of the requests ahead of this pass
         for (int r0 = 0; r0 < p.B && before <= start; r0 += kThreads) {
             const int r = r0 + tid;
-            const int64_t own = r < p.B ? units_of(p, request_of(p, r)) : 0;
+            const int64_t own = r < p.B ? units_of<S>(p, request_of<S>(p, r)) : 0;
             int64_t incl = own;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -409,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
     }
     __syncthreads();
 
-    Walk wk;
+    Walk<S> wk;
     if (count > 0) wk.start(p, hd.start_r, hd.start_off, count);
 
     if (count > 0 && warp == kLoadWarp) {
@@ -419,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         const int boxes = per_tile * (D / 64);           // at most 8 * 4
         const int my_page = lane % per_tile, my_col = lane / per_tile;
         uint32_t n = 0;                                  // slots filled so far
+        Place<S::kSlots> to{0, 0};                       // the next one
         bool ok = true;
         for (; ok && wk.valid(); wk.next(p)) {
             const int32_t *table = p.table + int64_t(wk.r) * p.max_pages;
@@ -442,17 +527,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                 if (page >= 0 && page < p.pages && x < wk.q.end)
                     y = ((page * p.Hkv + wk.h) << p.page_shift) + int32_t(x & ((1 << p.page_shift) - 1));
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const int s = n % S::kSlots;
-                    if (!warp_wait(empty(s), ((n / S::kSlots) & 1) ^ 1, failed, p.limit_ns)) {
+                for (int part = 0; part < (S::kPair ? 1 : 2); ++part, ++n) {
+                    const uint32_t s = to.at;
+                    if (!warp_wait(empty(s), to.phase ^ 1, failed, p.limit)) {
                         ok = false;
                         break;
                     }
+                    to.step(1);
                     if (lane == 0) mbar_expect_tx(full(s), S::kSlotBytes);
                     __syncwarp();
-                    if (lane < boxes)
-                        tma_load(slots + s * S::kSlotBytes + my_col * (kTile * 128) + my_page * box_rows * 128,
-                                 kv ? &p.v_map : &p.k_map, my_col * 64, y, full(s));
+                    const uint32_t dst = slots + s * S::kSlotBytes + my_col * (kTile * 128) + my_page * box_rows * 128;
+                    if (lane < boxes) {
+                        tma_load(dst, part ? &p.v_map : &p.k_map, my_col * 64, y, full(s));
+                        if (S::kPair) tma_load(dst + S::kTileBytes, &p.v_map, my_col * 64, y, full(s));
+                    }
                 }
             }
         }
@@ -467,45 +555,64 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
     } else if (count > 0 && warp == kMmaWarp) {
         // ---- products, by one thread ----
         if (lane == 0) {
+            // (an instruction at a time: places and phases are carried along, and descriptors
+            // differ in their low words only)
             constexpr uint32_t kQk = instr_desc<T>(kTile, false), kPv = instr_desc<T>(D, true);
-            uint32_t it = 0, item = 0;                   // tiles and items so far
-            bool ok = true;
-            auto pv = [&](uint32_t k, bool first) {      // tile k's P V into O
-                const uint32_t n = 2 * k + 1;
-                const int s = n % S::kSlots;
-                ok = wait(smem_addr(&hd.p_ready[k & 1]), (k >> 1) & 1, failed, p.limit_ns) &&
-                     wait(full(s), (n / S::kSlots) & 1, failed, p.limit_ns);
+            constexpr uint32_t kSlotStep = S::kSlotBytes / 16;
+            const uint64_t q_desc = operand_desc(q_smem, 16, 1024), k_desc = operand_desc(slots, 16, 1024);
+            const uint64_t v_desc = operand_desc(slots + (S::kPair ? S::kTileBytes : 0), kTile * 128, 1024);
+            const uint32_t q_lo = uint32_t(q_desc), q_hi = uint32_t(q_desc >> 32);
+            const uint32_t k_lo = uint32_t(k_desc), k_hi = uint32_t(k_desc >> 32);
+            const uint32_t v_lo = uint32_t(v_desc), v_hi = uint32_t(v_desc >> 32);
+            auto desc = [](uint32_t hi, uint32_t lo) { return (uint64_t(hi) << 32) | lo; };
+            Place<S::kSlots> k_at{0, 0}, v_at{S::kPair ? 0u : 1u, 0};    // the next K and V slots
+            Place<S::kBufs> s_at{0, 0}, p_at{0, 0};      // the next S tile to write, the next P to use
+            uint32_t item = 0;
+            bool ok = true, used = false;                // used: S tiles have been round once
+            auto pv = [&](bool first) {                  // the next tile's P V into O
+                ok = wait(smem_addr(&hd.p_ready[p_at.at]), p_at.phase, failed, p.limit) &&
+                     (S::kPair || wait(full(v_at.at), v_at.phase, failed, p.limit));
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t v = slots + s * S::kSlotBytes;
+                const uint32_t lo = v_lo + v_at.at * kSlotStep, a = tmem + S::kP + p_at.at * S::kPStep;
 #pragma unroll
-                for (int j = 0; j < kTile / 16; ++j)
-                    tc_mma_ts(tmem + S::kO, tmem + (k & 1) * kTile + j * 8, operand_desc(v + j * 2048, kTile * 128, 1024),
-                              kPv, !(first && j == 0));
-                tc_commit(empty(s));
-                tc_commit(smem_addr(&hd.pv_done[k & 1]));
+                for (int j = 0; j < kTile / 16; ++j) {
+                    if (REP == 1) {
+                        tc_mma_ts(tmem + S::kO, a + j * 8, desc(v_hi, lo + j * 128), kPv, !(first && j == 0));
+                    } else {                             // these 16 positions: into their copy's lanes
+                        constexpr int kSteps = kTile / 16 / REP, kQuads = kSoftWarps / REP;
+                        tc_mma_ts_quads(tmem + S::kO, a + j * 8, desc(v_hi, lo + j * 128), kPv,
+                                        !(first && j % kSteps == 0), ((1u << kQuads) - 1) << (j / kSteps * kQuads));
+                    }
+                }
+                tc_commit(empty(v_at.at));
+                tc_commit(smem_addr(&hd.pv_done[p_at.at]));
+                v_at.step(S::kPair ? 1 : 2);
+                p_at.step(1);
             };
             for (; ok && wk.valid(); wk.next(p), ++item) {
-                ok = wait(smem_addr(&hd.q_ready), item & 1, failed, p.limit_ns);
-                for (int t = wk.a; ok && t < wk.b; ++t, ++it) {
-                    const uint32_t n = 2 * it;
-                    const int s = n % S::kSlots;
-                    // K is there, and P of two tiles ago, which S overwrites, has been used
-                    ok = wait(full(s), (n / S::kSlots) & 1, failed, p.limit_ns) &&
-                         (it < 2 || wait(smem_addr(&hd.pv_done[it & 1]), ((it >> 1) - 1) & 1, failed, p.limit_ns));
+                ok = wait(smem_addr(&hd.q_ready), item & 1, failed, p.limit);
+                for (int t = wk.a; ok && t < wk.b; ++t) {
+                    // K is there, and the S of kBufs tiles ago has been read; where P lies over S,
+                    // its product is over too
+                    ok = wait(full(k_at.at), k_at.phase, failed, p.limit) &&
+                         (!used || wait(S::kOwnP ? smem_addr(&hd.s_free) : smem_addr(&hd.pv_done[s_at.at]),
+                                        s_at.phase ^ 1, failed, p.limit));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t k = slots + s * S::kSlotBytes;
+                    const uint32_t lo = k_lo + k_at.at * kSlotStep, d = tmem + s_at.at * kTile;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j)
-                        tc_mma_ss(tmem + (it & 1) * kTile,
-                                  operand_desc(q_smem + (j / 4) * (kRows * 128) + (j % 4) * 32, 16, 1024),
-                                  operand_desc(k + (j / 4) * (kTile * 128) + (j % 4) * 32, 16, 1024), kQk, j > 0);
-                    tc_commit(empty(s));
-                    tc_commit(smem_addr(&hd.s_full[it & 1]));
-                    if (t > wk.a) pv(it - 1, t - 1 == wk.a);
+                        tc_mma_ss(d, desc(q_hi, q_lo + (j / 4) * (kRows * 8) + (j % 4) * 2),
+                                  desc(k_hi, lo + (j / 4) * (kTile * 8) + (j % 4) * 2), kQk, j > 0);
+                    if (!S::kPair) tc_commit(empty(k_at.at));
+                    tc_commit(smem_addr(&hd.s_full[s_at.at]));
+                    k_at.step(S::kPair ? 1 : 2);
+                    s_at.step(1);
+                    used = used || s_at.phase;
+                    if (t - wk.a >= S::kAhead) pv(t - S::kAhead == wk.a);
                 }
-                if (ok) pv(it - 1, wk.b - 1 == wk.a);
+                for (int left = min(S::kAhead, wk.b - wk.a); ok && left > 0; --left) pv(wk.b - left == wk.a);
             }
             {                                            // nor does a product
                 tc_commit(smem_addr(&hd.drain));
@@ -516,21 +623,30 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         }
         __syncwarp();
     } else if (warp < kSoftWarps) {
-        // ---- softmax: a thread per row ----
+        // ---- softmax: a thread per row, or REP threads in as many warps, each for its
+        // kCols columns of every tile ----
+        constexpr int kQuads = kSoftWarps / REP, kCols = kTile / REP;    // warps of a copy; columns of a thread
         const uint32_t lanes = uint32_t(warp * 32) << 16;
-        const int row = warp * 32 + lane;
-        uint32_t it = 0, item = 0;
+        const int copy = warp / kQuads, col0 = copy * kCols;
+        const int row = (warp % kQuads) * 32 + lane, thread = warp * 32 + lane;
+        uint32_t it = 0, item = 0, syncs = 0;
+        Place<S::kBufs> s_at{0, 0}, before{0, 0};        // this tile's S, and the last tile's
+        // all the threads here, false on failure
+        auto soft_sync = [&]() {
+            mbar_arrive(smem_addr(&hd.sync));
+            return warp_wait(smem_addr(&hd.sync), syncs++ & 1, failed, p.limit);
+        };
         unsigned char *stage = smem + kBarBytes + warp * 4096;       // 32 rows of 128 bytes, in Q's place
         Meta meta{-1, 0, 0, 0, 0, 0, 0, 0};
         bool ok = true;
         // rows of the block past q_len, and those of requests that see nothing
         for (int r = cta; r < p.B; r += p.ctas) {
-            const Request q = request_of(p, r);
+            const Request q = request_of<S>(p, r);
             const int64_t i0 = (int64_t(r) * p.N + (q.nt ? q.n : 0)) * p.Hq, i1 = int64_t(r + 1) * p.N * p.Hq;
-            for (int64_t x = i0 * (D / 8) + row; x < i1 * (D / 8); x += kRows)
+            for (int64_t x = i0 * (D / 8) + thread; x < i1 * (D / 8); x += kRows)
                 reinterpret_cast<uint4 *>(p.out)[x] = make_uint4(0, 0, 0, 0);
             if (p.lse)
-                for (int64_t x = i0 + row; x < i1; x += kRows) p.lse[x] = -INFINITY;
+                for (int64_t x = i0 + thread; x < i1; x += kRows) p.lse[x] = -INFINITY;
         }
         for (; count > 0 && ok && wk.valid(); wk.next(p), ++item) {
             const Request &q = wk.q;
@@ -542,26 +658,32 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             // Q, 16 bytes at a time, where the products' swizzle wants it, all copies in
             // flight together (idle rows keep what was there: a row of S depends on its own
             // row of Q only).  Before it, the last item's result has left these bytes.
-            if (item > 0 && !warp_wait(smem_addr(&hd.staged), (item - 1) & 1, failed, p.limit_ns)) {
+            if (item > 0 && !warp_wait(smem_addr(&hd.staged), (item - 1) & 1, failed, p.limit)) {
                 ok = false;
                 break;
             }
             {
                 constexpr int kCh = D / 8, kStep = kRows / kCh;          // chunks of a row, rows of a pass
-                const int ch = row % kCh;
+                const int ch = thread % kCh;
                 const T *src = static_cast<const T *>(p.q) + wk.r * p.qb + wk.h * p.G * p.qh + ch * 8;
                 unsigned char *dst = smem + kBarBytes + (ch >> 3) * (kRows * 128);
-                for (int y = row / kCh; y < rows; y += kStep) {
+                for (int y = thread / kCh; y < rows; y += kStep) {
                     const uint32_t ry = wk.mt * kRows + y, iy = ry / uint32_t(p.G);
-                    copy16(smem_addr(dst + y * 128 + (((ch & 7) ^ (y & 7)) << 4)),
-                           src + iy * p.qn + (ry - iy * p.G) * p.qh);
+#pragma unroll
+                    for (int k = 0; k < REP; ++k)
+                        copy16(smem_addr(dst + (y + k * kQuads * 32) * 128 + (((ch & 7) ^ (y & 7)) << 4)),
+                               src + iy * p.qn + (ry - iy * p.G) * p.qh);
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 if (p.negate)
-                    for (int y = row / kCh; y < rows; y += kStep) {
-                        uint4 *v = reinterpret_cast<uint4 *>(dst + y * 128 + (((ch & 7) ^ (y & 7)) << 4));
-                        *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u, v->w ^ 0x80008000u);
-                    }
+                    for (int y = thread / kCh; y < rows; y += kStep)
+#pragma unroll
+                        for (int k = 0; k < REP; ++k) {
+                            uint4 *v = reinterpret_cast<uint4 *>(dst + (y + k * kQuads * 32) * 128 +
+                                                                 (((ch & 7) ^ (y & 7)) << 4));
+                            *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u,
+                                            v->w ^ 0x80008000u);
+                        }
                 lkd::fence_proxy_async_smem();
                 mbar_arrive(smem_addr(&hd.q_ready));
             }
@@ -570,108 +692,143 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             const int64_t see1 = min(pos + 1, q.end);
             const int64_t see0 = p.window > 0 ? max(pos - p.window + 1, int64_t(0)) : 0;
             float m = -INFINITY, sum = 0.0f;             // m: the raw product the sums are relative to
-            const bool warp_live = warp * 32 < rows;
+            const bool warp_live = (warp % kQuads) * 32 < rows;
             for (int t = wk.a; t < wk.b; ++t, ++it) {
                 const int64_t x0 = int64_t(q.t0 + t) * kTile;
-                if (!warp_wait(smem_addr(&hd.s_full[it & 1]), (it >> 1) & 1, failed, p.limit_ns)) {
+                const uint32_t buf = s_at.at;
+                if (!warp_wait(smem_addr(&hd.s_full[buf]), s_at.phase, failed, p.limit)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (x0 < q.lo || x0 + kTile > q.end) {
                     // rows of V that no row of the block sees may hold anything: zeros
-                    const uint32_t n = 2 * it + 1;
+                    const uint32_t n = S::kPair ? it : 2 * it + 1;
                     const int s = n % S::kSlots;
-                    if (!warp_wait(full(s), (n / S::kSlots) & 1, failed, p.limit_ns)) {
+                    if (!warp_wait(full(s), (n / S::kSlots) & 1, failed, p.limit)) {
                         ok = false;
                         break;
                     }
-                    unsigned char *v = smem + kBarBytes + S::kQBytes + s * S::kSlotBytes;
-                    for (int x = row; x < kTile * (D / 8); x += kRows) {
+                    unsigned char *v = smem + kBarBytes + S::kQBytes + s * S::kSlotBytes + (S::kPair ? S::kTileBytes : 0);
+                    for (int x = thread; x < kTile * (D / 8); x += kRows) {
                         const int y = (x >> 3) & (kTile - 1);
                         if (x0 + y < q.lo || x0 + y >= q.end)
                             *reinterpret_cast<uint4 *>(v + x * 16) = make_uint4(0, 0, 0, 0);
                     }
                     lkd::fence_proxy_async_smem();
                 }
+                const bool fresh = t == wk.a;
                 if (warp_live) {
-                    const uint32_t at = tmem + lanes + (it & 1) * kTile;
-                    uint32_t r0[32], r1[32];
-                    tc_ld32(at, r0);
-                    tc_ld32(at + 32, r1);
-                    tc_wait_ld(r0);
-                    tc_wait_ld(r1);
+                    // a thread's columns, 32 (or its 16) at a time; 64 stay in registers, 128 are
+                    // read twice, for the maximum and for the weights
+                    constexpr int kStep = kCols < 32 ? kCols : 32, kSteps = kCols / kStep;
+                    constexpr bool kTwice = kCols > 64;
+                    const uint32_t at = tmem + lanes + buf * kTile + col0;
+                    uint32_t r[kTwice ? 1 : kSteps][kStep];
                     // tiles that some row of the request sees less than all of
                     const bool masked = x0 + kTile > min(int64_t(q.kv) + 1, q.end) ||
                                         (p.window > 0 && x0 < int64_t(q.kv) + q.n - p.window);
-                    if (masked) {
-                        const int c0 = int(min(max(see0 - x0, int64_t(0)), int64_t(kTile)));
-                        const int c1 = int(min(max(see1 - x0, int64_t(0)), int64_t(kTile)));
+                    const int c0 = int(min(max(see0 - x0, int64_t(0)), int64_t(kTile))) - col0;
+                    const int c1 = int(min(max(see1 - x0, int64_t(0)), int64_t(kTile))) - col0;
+                    auto hide = [&](uint32_t (&x)[kStep], int from) {
+                        if (!masked) return;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if (j < c0 || j >= c1) r0[j] = 0xff800000u;
-                            if (j + 32 < c0 || j + 32 >= c1) r1[j] = 0xff800000u;
+                        for (int j = 0; j < kStep; ++j)
+                            if (from + j < c0 || from + j >= c1) x[j] = 0xff800000u;
+                    };
+                    float mx = -INFINITY;
+                    if (!kTwice) {
+#pragma unroll
+                        for (int h = 0; h < kSteps; ++h) tc_ld(at + h * kStep, r[kTwice ? 0 : h]);
+#pragma unroll
+                        for (int h = 0; h < kSteps; ++h) tc_wait_ld(r[kTwice ? 0 : h]);
+                        if (S::kOwnP) {                  // S is in registers: the next may come
+                            tc_fence_before();
+                            mbar_arrive(smem_addr(&hd.s_free));
                         }
                     }
-                    float mx = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fmaxf(__uint_as_float(r0[j]), __uint_as_float(r1[j])));
-                    const bool fresh = t == wk.a;
-                    bool lift = mx > m && (fresh || m == -INFINITY || (mx - m) * p.c > kLazy);
-                    if (fresh) {
-                        m = mx;
-                    } else if (__any_sync(0xffffffffu, lift)) {
-                        // bring O and the sum to the new m; P V of the tile before has to be in O
-                        if (!warp_wait(smem_addr(&hd.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, failed, p.limit_ns)) {
+                    for (int h = 0; h < kSteps; ++h) {
+                        uint32_t (&x)[kStep] = r[kTwice ? 0 : h];
+                        if (kTwice) {
+                            tc_ld(at + h * kStep, x);
+                            tc_wait_ld(x);
+                        }
+                        hide(x, h * kStep);
+#pragma unroll
+                        for (int j = 0; j < kStep; j += 2)
+                            mx = fmaxf(mx, fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
+                    }
+                    const bool lift = mx > m && (fresh || m == -INFINITY || (mx - m) * p.c > kLazy);
+                    // the last product is over: before O is brought to a new m, and before P is
+                    // overwritten where there is one
+                    if ((S::kOwnP && it > 0) || (!fresh && __any_sync(0xffffffffu, lift))) {
+                        if (!warp_wait(smem_addr(&hd.pv_done[before.at]), before.phase, failed, p.limit)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
+                    }
+                    if (fresh) {
+                        m = mx;
+                    } else if (__any_sync(0xffffffffu, lift)) {
                         const float f = !lift ? 1.0f : (m == -INFINITY ? 0.0f : exp2_approx((m - mx) * p.c));
                         if (lift) m = mx;
                         sum *= f;
 #pragma unroll
                         for (int j = 0; j < D; j += 32) {
                             uint32_t o[32];
-                            tc_ld32(tmem + lanes + S::kO + j, o);
+                            tc_ld(tmem + lanes + S::kO + j, o);
                             tc_wait_ld(o);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
                                 o[k] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(o[k]) * f);
-                            tc_st32(tmem + lanes + S::kO + j, o);
+                            tc_st(tmem + lanes + S::kO + j, o);
                         }
                     }
                     const float mc = m == -INFINITY ? 0.0f : m * p.c;
-                    float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-                    uint32_t w[32];
+                    float part_sum[4] = {};
+                    const uint32_t to = tmem + lanes + S::kP + buf * S::kPStep + copy * (kCols / 2);
+                    uint32_t w[kTwice ? kStep / 2 : kCols / 2];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float x0f = __uint_as_float(r0[j]), x1f = __uint_as_float(r0[j + 1]);
-                        const float y0f = __uint_as_float(r1[j]), y1f = __uint_as_float(r1[j + 1]);
-                        float a0 = exp2_approx(fmaf(x0f, p.c, -mc)), a1 = exp2_approx(fmaf(x1f, p.c, -mc));
-                        float b0 = exp2_approx(fmaf(y0f, p.c, -mc)), b1 = exp2_approx(fmaf(y1f, p.c, -mc));
-                        if (masked) {                    // also where c is 0
-                            a0 = r0[j] == 0xff800000u ? 0.0f : a0;
-                            a1 = r0[j + 1] == 0xff800000u ? 0.0f : a1;
-                            b0 = r1[j] == 0xff800000u ? 0.0f : b0;
-                            b1 = r1[j + 1] == 0xff800000u ? 0.0f : b1;
+                    for (int h = 0; h < kSteps; ++h) {
+                        uint32_t (&x)[kStep] = r[kTwice ? 0 : h];
+                        if (kTwice) {
+                            tc_ld(at + h * kStep, x);
+                            tc_wait_ld(x);
+                            if (h == kSteps - 1 && S::kOwnP) {
+                                tc_fence_before();
+                                mbar_arrive(smem_addr(&hd.s_free));
+                            }
+                            hide(x, h * kStep);
                         }
-                        s0 += a0;
-                        s1 += a1;
-                        s2 += b0;
-                        s3 += b1;
-                        w[j / 2] = pack2(a0, a1, T());
-                        w[16 + j / 2] = pack2(b0, b1, T());
+#pragma unroll
+                        for (int j = 0; j < kStep; j += 2) {
+                            float a0 = exp2_approx(fmaf(__uint_as_float(x[j]), p.c, -mc));
+                            float a1 = exp2_approx(fmaf(__uint_as_float(x[j + 1]), p.c, -mc));
+                            if (masked) {                // also where c is 0
+                                a0 = x[j] == 0xff800000u ? 0.0f : a0;
+                                a1 = x[j + 1] == 0xff800000u ? 0.0f : a1;
+                            }
+                            part_sum[j & 2] += a0;
+                            part_sum[(j & 2) + 1] += a1;
+                            w[(kTwice ? 0 : h * kStep / 2) + j / 2] = pack2(a0, a1, T());
+                        }
+                        if (kTwice) tc_st(to + h * (kStep / 2), w);
                     }
-                    sum += (s0 + s1) + (s2 + s3);
-                    tc_st32(at, w);
+                    sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+                    if (!kTwice) tc_st(to, w);
                     tc_wait_st();
+                } else if (S::kOwnP) {
+                    mbar_arrive(smem_addr(&hd.s_free));
                 }
                 tc_fence_before();
-                mbar_arrive(smem_addr(&hd.p_ready[it & 1]));
+                mbar_arrive(smem_addr(&hd.p_ready[buf]));
+                before = s_at;
+                s_at.step(1);
             }
             if (!ok) break;
-            if (!warp_wait(smem_addr(&hd.pv_done[(it - 1) & 1]), ((it - 1) >> 1) & 1, failed, p.limit_ns)) {
+            if (!warp_wait(smem_addr(&hd.pv_done[before.at]), before.phase, failed, p.limit)) {
                 ok = false;
                 break;
             }
@@ -681,7 +838,85 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             // pieces swizzled by the row), so that whole lines are written.
             const bool whole = wk.a == 0 && wk.b == q.nt;
             const int my_row = lane >> 3, my_piece = lane & 7;       // of four rows at a time
-            if (whole) {
+            // slot 2c + 1: the item began here; 2c: it began in an earlier range
+            const int slot = 2 * cta + (wk.a == 0 ? 1 : 0);
+            float *ws = p.parts + int64_t(slot) * (D + 2) * p.part_rows;
+            if (REP > 1) {
+                // the copies' sums added: each at the largest of their m, every copy a part of the rows
+                float f = 0.0f, all = 0.0f, big = -INFINITY;
+                float *own = reinterpret_cast<float *>(stage);
+                own[lane] = m;
+                own[32 + lane] = sum;
+                if (!(ok = soft_sync())) break;
+                const float *first = reinterpret_cast<const float *>(smem + kBarBytes + (warp % kQuads) * 4096);
+#pragma unroll
+                for (int k = 0; k < REP; ++k)
+                    if (first[k * kQuads * 1024 + 32 + lane] != 0.0f) big = fmaxf(big, first[k * kQuads * 1024 + lane]);
+#pragma unroll
+                for (int k = 0; k < REP; ++k) {
+                    const float mk = first[k * kQuads * 1024 + lane], sk = first[k * kQuads * 1024 + 32 + lane];
+                    const float w = sk == 0.0f ? 0.0f : mk == big ? 1.0f : exp2_approx((mk - big) * p.c);
+                    if (w != 0.0f) all += w * sk;
+                    if (k == copy) f = w;
+                }
+                if (!(ok = soft_sync())) break;
+                if (whole) f = all == 0.0f ? 0.0f : f / all;
+#pragma unroll
+                for (int j = 0; j < D; j += 32) {
+                    if (warp_live) {
+                        uint32_t o[32];
+                        tc_ld(tmem + lanes + S::kO + j, o);
+                        tc_wait_ld(o);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[4 * k + e]) * f);
+                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                                make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
+                    if (!(ok = soft_sync())) break;
+#pragma unroll
+                    for (int t = 0; t < 32 / REP; t += 4) {
+                        const int y = copy * (32 / REP) + t + my_row, full_y = (warp % kQuads) * 32 + y;
+                        if (full_y < rows) {
+                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                            for (int k = 0; k < REP; ++k) {
+                                const float4 u = *reinterpret_cast<const float4 *>(
+                                    smem + kBarBytes + (warp % kQuads + k * kQuads) * 4096 + y * 128 +
+                                    ((my_piece ^ (y & 7)) << 4));
+                                v.x += u.x;
+                                v.y += u.y;
+                                v.z += u.z;
+                                v.w += u.w;
+                            }
+                            if (whole) {
+                                const uint32_t ry = wk.mt * kRows + full_y, iy = ry / uint32_t(p.G);
+                                const int64_t o_row =
+                                    (int64_t(wk.r) * p.N + iy) * p.Hq + wk.h * p.G + (ry - iy * uint32_t(p.G));
+                                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + o_row * D + j + my_piece * 4) =
+                                    make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
+                            } else {
+                                *reinterpret_cast<float4 *>(ws + full_y * D + j + my_piece * 4) = v;
+                            }
+                        }
+                    }
+                    if (!(ok = soft_sync())) break;
+                }
+                if (!ok) break;
+                if (live && copy == 0) {
+                    if (!whole) {
+                        ws[D * p.part_rows + row] = big;
+                        ws[(D + 1) * p.part_rows + row] = all;
+                    } else if (p.lse) {
+                        p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
+                            all == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(all));
+                    }
+                }
+            } else if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 if (warp_live) {
 #pragma unroll
@@ -689,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             uint32_t o[32];
-                            tc_ld32(tmem + lanes + S::kO + j + 32 * half, o);
+                            tc_ld(tmem + lanes + S::kO + j + 32 * half, o);
                             tc_wait_ld(o);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -722,14 +957,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                             sum == 0.0f ? -INFINITY : 0.6931471805599453f * (m * p.c + log2f(sum));
                 }
             } else {
-                // slot 2c + 1: the item began here; 2c: it began in an earlier range
-                const int slot = 2 * cta + (wk.a == 0 ? 1 : 0);
-                float *ws = p.parts + int64_t(slot) * (D + 2) * p.part_rows;
                 if (warp_live) {
 #pragma unroll
                     for (int j = 0; j < D; j += 32) {
                         uint32_t o[32];
-                        tc_ld32(tmem + lanes + S::kO + j, o);
+                        tc_ld(tmem + lanes + S::kO + j, o);
                         tc_wait_ld(o);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -750,6 +982,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         ws[(D + 1) * p.part_rows + row] = sum;
                     }
                 }
+            }
+            if (!whole) {
                 if (wk.a == 0) {
                     // the CTA that has the item's last unit: the largest c whose range starts at or before it
                     const int64_t end = stop + (q.nt - wk.b);            // of the item's units
@@ -762,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             tc_fence_before();                           // O is read before the next item's products (p_ready)
             mbar_arrive(smem_addr(&hd.staged));
         }
-        if (row == 0) {
+        if (thread == 0) {
             meta.failed = ok ? 0 : 1;
             p.meta[cta] = meta;
         }
@@ -775,32 +1009,25 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
     if (tid == 0 && hd.failed) p.meta[cta].failed = 1;
 }
 
-// Joins the parts of the item that CTA blockIdx.x of attention_kernel began and did
-// not end.  Few parts (many items, each cut once or twice): a warp per row, the parts'
-// maxima, sums and rows loaded together.  Many (few long items): kJoinRows rows at a
-// time, first their weights 2^(c (m_k - M)), a warp per row and a lane per part; then
-// each warp sums every eighth part over those rows, and the warps' sums are added.  A wait that ran out anywhere makes the whole call's rows NaN.
+template <int D>
+struct JoinSmem {
+    static constexpr int kMost = kMaxSms * Shape<D>::kCtas;          // parts at most
+    float weights[kJoinRows][kMost], parts[kJoinRows][kMost], big[kJoinRows], sum[kJoinRows];
+    float sums[kJoinWarps][kJoinRows][D];
+    Meta metas[kMost];
+};
+
+// Joins the parts of the item that CTA c of attention_kernel began and did not end, the
+// rows of this CTA's blockIdx.y.  Few parts (many items, each cut once or twice): a warp
+// per row, the parts' maxima, sums and rows loaded together.  Many (few long items):
+// kJoinRows rows at a time, first their weights 2^(c (m_k - M)), a warp per row and a
+// lane per part; then each warp sums every eighth part over those rows, and the warps'
+// sums are added.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 4) join_kernel(const __grid_constant__ Params p) {
+__device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> &sm) {
     constexpr int E = D / 32;                            // columns of a lane
-    __shared__ float weights[kJoinRows][kMaxCtas], s_big[kJoinRows], s_sum[kJoinRows];
-    __shared__ float sums[kJoinWarps][kJoinRows][D];
-    wait_for_prerequisite_grid();
-    allow_dependent_launch();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
-    const Meta meta = p.meta[c];
-    int bad = 0;
-    for (int k = tid; k < p.ctas; k += kJoinThreads) bad |= p.meta[k].failed;
-    if (__syncthreads_or(bad)) {
-        const int64_t rows = int64_t(p.B) * p.N * p.Hq;
-        const int64_t first = (int64_t(blockIdx.y) * gridDim.x + c) * kJoinThreads + tid;
-        const int64_t step = int64_t(gridDim.x) * gridDim.y * kJoinThreads;
-        for (int64_t x = first; x < rows * D; x += step) static_cast<T *>(p.out)[x] = T(NAN);
-        if (p.lse)
-            for (int64_t x = first; x < rows; x += step) p.lse[x] = NAN;
-        return;
-    }
-    if (meta.r < 0) return;
+    constexpr int kFirst = D == 64 ? 4 : D == 128 ? 2 : 1;           // parts of a warp in flight
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t size = int64_t(D + 2) * p.part_rows;   // of a part
     const int count = meta.last - c + 1;
     const float *own = p.parts + int64_t(2 * c + 1) * size, *more = own + size;    // the first, then every second
@@ -852,13 +1079,26 @@ __global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 4) join_kernel(co
     }
     for (int row0 = blockIdx.y * kJoinRows; row0 < meta.rows; row0 += gridDim.y * kJoinRows) {
         const int rows = min(kJoinRows, meta.rows - row0);
+        // the warp's first parts on their way while the weights are worked out
+        float2 v[kFirst][kJoinRows][E / 2];
+        auto fetch = [&](float2 (&to)[kJoinRows][E / 2], int k) {
+            const float2 *src = reinterpret_cast<const float2 *>(part(k) + row0 * D + lane * E);
+#pragma unroll
+            for (int y = 0; y < kJoinRows; ++y)
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e)
+                    to[y][e] = k < count && y < rows ? src[y * (D / 2) + e] : make_float2(0.0f, 0.0f);
+        };
+#pragma unroll
+        for (int f = 0; f < kFirst; ++f) fetch(v[f], warp + f * kJoinWarps);
         if (warp < rows) {
             const int row = row0 + warp;
-            float *weight = weights[warp];
+            float *weight = sm.weights[warp];
             float big = -INFINITY, sum = 0.0f;
             for (int k = lane; k < count; k += 32) {
                 const float mk = part(k)[D * p.part_rows + row], sk = part(k)[(D + 1) * p.part_rows + row];
                 weight[k] = sk == 0.0f ? -INFINITY : mk;
+                sm.parts[warp][k] = sk;
                 if (sk != 0.0f) big = fmaxf(big, mk);
             }
 #pragma unroll
@@ -867,51 +1107,78 @@ __global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 4) join_kernel(co
                 const float mk = weight[k];
                 const float w = mk == -INFINITY ? 0.0f : exp2f((mk - big) * p.c);
                 weight[k] = w;
-                if (w != 0.0f) sum += w * part(k)[(D + 1) * p.part_rows + row];
+                if (w != 0.0f) sum += w * sm.parts[warp][k];
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             if (lane == 0) {
-                s_big[warp] = big;
-                s_sum[warp] = sum;
+                sm.big[warp] = big;
+                sm.sum[warp] = sum;
             }
         }
         __syncthreads();
         float o[kJoinRows][E] = {};
-#pragma unroll 2
-        for (int k = warp; k < count; k += kJoinWarps) {
-            const float2 *src = reinterpret_cast<const float2 *>(part(k) + row0 * D + lane * E);
-            float2 v[kJoinRows][E / 2];
+        for (int k = warp; k < count; k += kFirst * kJoinWarps) {
 #pragma unroll
-            for (int y = 0; y < kJoinRows; ++y)
+            for (int f = 0; f < kFirst; ++f) {
+                const int at = k + f * kJoinWarps;
+                if (at >= count) break;
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e) v[y][e] = y < rows ? src[y * (D / 2) + e] : make_float2(0.0f, 0.0f);
+                for (int y = 0; y < kJoinRows; ++y) {
+                    const float w = y < rows ? sm.weights[y][at] : 0.0f;
 #pragma unroll
-            for (int y = 0; y < kJoinRows; ++y) {
-                const float w = y < rows ? weights[y][k] : 0.0f;
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e) {
-                    o[y][2 * e] += w == 0.0f ? 0.0f : w * v[y][e].x;
-                    o[y][2 * e + 1] += w == 0.0f ? 0.0f : w * v[y][e].y;
+                    for (int e = 0; e < E / 2; ++e) {
+                        o[y][2 * e] += w == 0.0f ? 0.0f : w * v[f][y][e].x;
+                        o[y][2 * e + 1] += w == 0.0f ? 0.0f : w * v[f][y][e].y;
+                    }
                 }
             }
+#pragma unroll
+            for (int f = 0; f < kFirst; ++f) fetch(v[f], k + (kFirst + f) * kJoinWarps);
         }
         // the warps' sums; then warp y adds and finishes row y
 #pragma unroll
         for (int y = 0; y < kJoinRows; ++y)
 #pragma unroll
-            for (int e = 0; e < E; ++e) sums[warp][y][e * 32 + lane] = o[y][e];
+            for (int e = 0; e < E; ++e) sm.sums[warp][y][e * 32 + lane] = o[y][e];
         __syncthreads();
         if (warp < rows) {
             float all[E] = {};
 #pragma unroll
             for (int w = 0; w < kJoinWarps; ++w)
 #pragma unroll
-                for (int e = 0; e < E; ++e) all[e] += sums[w][warp][e * 32 + lane];
-            finish(row0 + warp, all, s_big[warp], s_sum[warp]);
+                for (int e = 0; e < E; ++e) all[e] += sm.sums[w][warp][e * 32 + lane];
+            finish(row0 + warp, all, sm.big[warp], sm.sum[warp]);
         }
         __syncthreads();                                 // shared memory has been read
     }
+}
+
+// The items that were cut: CTA x takes those begun by CTAs x, x + gridDim.x, ... of
+// attention_kernel.  A wait that ran out anywhere makes the whole call's rows NaN.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 4) join_kernel(const __grid_constant__ Params p) {
+    __shared__ JoinSmem<D> sm;
+    wait_for_prerequisite_grid();
+    allow_dependent_launch();
+    const int tid = threadIdx.x;
+    int bad = 0;
+    for (int k = tid; k < p.ctas; k += kJoinThreads) {
+        const Meta meta = p.meta[k];
+        bad |= meta.failed;
+        if (k % gridDim.x == blockIdx.x) sm.metas[k / gridDim.x] = meta;
+    }
+    if (__syncthreads_or(bad)) {
+        const int64_t rows = int64_t(p.B) * p.N * p.Hq;
+        const int64_t first = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * kJoinThreads + tid;
+        const int64_t step = int64_t(gridDim.x) * gridDim.y * kJoinThreads;
+        for (int64_t x = first; x < rows * D; x += step) static_cast<T *>(p.out)[x] = T(NAN);
+        if (p.lse)
+            for (int64_t x = first; x < rows; x += step) p.lse[x] = NAN;
+        return;
+    }
+    for (int c = blockIdx.x, k = 0; c < p.ctas; c += gridDim.x, ++k)
+        if (sm.metas[k].r >= 0) join_item<T, D>(p, c, sm.metas[k], sm);
 }
 
 // -------------------------------------------------------------------- host ----
@@ -963,8 +1230,10 @@ int cache_map(EncodeTiled fn, CUtensorMap *map, const void *base, int32_t type, 
 template <typename T, int D>
 int launch(Params &p, cudaStream_t stream) {
     using S = Shape<D>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    // rows that fit a half or a quarter of the tile are there twice or four times
+    const int64_t rows = int64_t(p.N) * p.G;
+    auto kernel = rows <= 32 ? attention_kernel<T, D, 4> : rows <= 64 ? attention_kernel<T, D, 2> : attention_kernel<T, D, 1>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "shared-memory opt-in");
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -976,14 +1245,18 @@ int launch(Params &p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t r = cudaLaunchKernelEx(&cfg, attention_kernel<T, D>, p);
+    cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, p);
     if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
     lookup_note_launch();
-    // CTAs per item in the join: with about as many items as CTAs each is cut once or
-    // twice and a few CTAs do; a few long items have tens of parts and take them all
+    // The join.  With about as many items as ranges each is cut once or twice, and a few
+    // CTAs an item do; a few long items have tens of parts and take more, and where those
+    // CTAs times the ranges would be several waves of mostly idle ones, fewer CTAs share
+    // the ranges (an odd number: evenly cut items begin at even distances).
     const int64_t items = int64_t(p.B) * p.Hkv * ((int64_t(p.N) * p.G + kRows - 1) / kRows);
     const int most = (p.part_rows + kJoinRows - 1) / kJoinRows;
-    cfg.gridDim = dim3(p.ctas, 3 * items >= p.ctas ? std::min(most, 4) : std::min(most, 16));
+    const int per = std::min(most, 3 * items >= p.ctas ? 4 : 16);
+    const int64_t over = int64_t(per) * p.ctas <= 1216 ? p.ctas : std::min<int64_t>(p.ctas, 2 * items + 1);
+    cfg.gridDim = dim3(unsigned(over), per);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     r = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p);
@@ -1019,7 +1292,7 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
         !(std::fabs(scale) < INFINITY) || (type != LOOKUP_TYPE_F16 && type != LOOKUP_TYPE_BF16))
         return LOOKUP_DRAFT_EINVAL;
     const int64_t cache_rows = int64_t(pages) * Hkv * page_size;
-    if (cache_rows > INT32_MAX - 2 * kTile || int64_t(max_pages) * page_size > INT32_MAX - 2 * kTile)
+    if (cache_rows > INT32_MAX - 128 || int64_t(max_pages) * page_size > INT32_MAX - 128)
         return LOOKUP_DRAFT_EINVAL;
     if (B == 0 || N == 0) return LOOKUP_DRAFT_OK;
     const int64_t rows = int64_t(B) * N * Hq;
@@ -1040,7 +1313,8 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
     Params p{};
     EncodeTiled fn = nullptr;
     rc = encode_fn(&fn);
-    const int box_rows = page_size < kTile ? page_size : kTile;
+    const int tile = D == 64 ? Shape<64>::kTile : D == 128 ? Shape<128>::kTile : Shape<256>::kTile;
+    const int box_rows = page_size < tile ? page_size : tile;
     if (rc == LOOKUP_DRAFT_OK) rc = cache_map(fn, &p.k_map, k_cache, type, D, cache_rows, box_rows);
     if (rc == LOOKUP_DRAFT_OK) rc = cache_map(fn, &p.v_map, v_cache, type, D, cache_rows, box_rows);
     if (rc != LOOKUP_DRAFT_OK) return rc;
@@ -1055,7 +1329,8 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
     p.out = out, p.lse = lse;
     p.meta = static_cast<Meta *>(workspace);
     p.parts = reinterpret_cast<float *>(p.meta + p.ctas);
-    p.limit_ns = lookup_wait_limit_ns();
+    p.limit = 2 * lookup_wait_limit_ns();        // at 2 GHz
+
     return type == LOOKUP_TYPE_F16 ? launch_d<__half>(p, D, stream) : launch_d<__nv_bfloat16>(p, D, stream);
 }
 
