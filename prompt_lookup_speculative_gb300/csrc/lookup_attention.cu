@@ -59,7 +59,6 @@ constexpr int kSoftWarps = 4;            // one thread per row
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kThreads = 192;
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;       // of a CTA of join_kernel
-constexpr int kJoinRows = 4;             // rows it joins at a time where an item has many parts
 constexpr int kFewParts = 4;             // parts that a warp joins by itself
 constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
 constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
@@ -93,7 +92,7 @@ struct Shape {
 
 struct Meta {                            // one per CTA: the item it began and did not end
     int32_t r, h, mt, last;              // r = -1: none; last = the CTA that ended it
-    int32_t rows, failed, pad0, pad1;
+    int32_t rows, failed, copies, pad;
 };
 
 struct Params {
@@ -107,7 +106,7 @@ struct Params {
     void *out;
     float *lse;
     Meta *meta;                          // [ctas]
-    float *parts;                        // [2 * ctas]: O [part_rows][D], m [part_rows], sum [part_rows]
+    float *parts;                        // [2 * ctas][copies]: O [part_rows][D], m [part_rows], sum [part_rows]
     uint64_t limit;                      // clocks that a wait may take
 };
 
@@ -448,14 +447,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
     wait_for_prerequisite_grid();
     allow_dependent_launch();
 
-    // the range of this CTA: units [start, stop) of all requests' units end to end
-    {
-        int64_t own = 0;
-        for (int r = tid; r < p.B; r += kThreads) own += units_of<S>(p, request_of<S>(p, r));
+    // the range of this CTA: units [start, stop) of all requests' units end to end.  A
+    // thread per request and a scan; more requests than threads take a second pass
+    auto scan = [&](int64_t x) {                         // over the warp, its total to warp_sum
 #pragma unroll
-        for (int d = 16; d; d >>= 1) own += __shfl_xor_sync(0xffffffffu, own, d);
-        if (lane == 0) hd.warp_sum[warp] = own;
-    }
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) hd.warp_sum[warp] = x;
+        return x;
+    };
+    int64_t own = 0;
+    for (int r = tid; r < p.B; r += kThreads) own += units_of<S>(p, request_of<S>(p, r));
+    int64_t upto = scan(own);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -470,24 +475,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         int64_t before = 0;                              // units of the requests ahead of this pass
         for (int r0 = 0; r0 < p.B && before <= start; r0 += kThreads) {
             const int r = r0 + tid;
-            const int64_t own = r < p.B ? units_of<S>(p, request_of<S>(p, r)) : 0;
-            int64_t incl = own;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += y;
+            if (p.B > kThreads) {
+                own = r < p.B ? units_of<S>(p, request_of<S>(p, r)) : 0;
+                __syncthreads();                         // warp_sum's last readers are done
+                upto = scan(own);
+                __syncthreads();
             }
-            __syncthreads();                             // warp_sum's last readers are done
-            if (lane == 31) hd.warp_sum[warp] = incl;
-            __syncthreads();
-            int64_t ahead = before;
+            int64_t ahead = before + upto - own;
             for (int w = 0; w < kThreads / 32; ++w) {
                 if (w < warp) ahead += hd.warp_sum[w];
                 before += hd.warp_sum[w];
             }
-            if (ahead + incl - own <= start && start < ahead + incl) {
+            if (ahead <= start && start < ahead + own) {
                 hd.start_r = r;
-                hd.start_off = start - (ahead + incl - own);
+                hd.start_off = start - ahead;
             }
         }
     }
@@ -496,6 +497,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
     Walk<S> wk;
     if (count > 0) wk.start(p, hd.start_r, hd.start_off, count);
 
+    if (warp == kMmaWarp) {
+        // rows of the block past q_len, and those of requests that see nothing (this warp
+        // has time: Q takes 2 us to come)
+        for (int r = cta; r < p.B; r += p.ctas) {
+            const Request q = request_of<S>(p, r);
+            const int64_t i0 = (int64_t(r) * p.N + (q.nt ? q.n : 0)) * p.Hq, i1 = int64_t(r + 1) * p.N * p.Hq;
+            for (int64_t x = i0 * (D / 8) + lane; x < i1 * (D / 8); x += 32)
+                reinterpret_cast<uint4 *>(p.out)[x] = make_uint4(0, 0, 0, 0);
+            if (p.lse)
+                for (int64_t x = i0 + lane; x < i1; x += 32) p.lse[x] = -INFINITY;
+        }
+    }
     if (count > 0 && warp == kLoadWarp) {
         // ---- loads: K and V of tile after tile, slot after slot ----
         const int box_rows = min(kTile, 1 << p.page_shift);
@@ -639,15 +652,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         unsigned char *stage = smem + kBarBytes + warp * 4096;       // 32 rows of 128 bytes, in Q's place
         Meta meta{-1, 0, 0, 0, 0, 0, 0, 0};
         bool ok = true;
-        // rows of the block past q_len, and those of requests that see nothing
-        for (int r = cta; r < p.B; r += p.ctas) {
-            const Request q = request_of<S>(p, r);
-            const int64_t i0 = (int64_t(r) * p.N + (q.nt ? q.n : 0)) * p.Hq, i1 = int64_t(r + 1) * p.N * p.Hq;
-            for (int64_t x = i0 * (D / 8) + thread; x < i1 * (D / 8); x += kRows)
-                reinterpret_cast<uint4 *>(p.out)[x] = make_uint4(0, 0, 0, 0);
-            if (p.lse)
-                for (int64_t x = i0 + thread; x < i1; x += kRows) p.lse[x] = -INFINITY;
-        }
         for (; count > 0 && ok && wk.valid(); wk.next(p), ++item) {
             const Request &q = wk.q;
             const int rows = min(kRows, q.n * p.G - wk.mt * kRows);
@@ -840,9 +844,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             const int my_row = lane >> 3, my_piece = lane & 7;       // of four rows at a time
             // slot 2c + 1: the item began here; 2c: it began in an earlier range
             const int slot = 2 * cta + (wk.a == 0 ? 1 : 0);
-            float *ws = p.parts + int64_t(slot) * (D + 2) * p.part_rows;
-            if (REP > 1) {
-                // the copies' sums added: each at the largest of their m, every copy a part of the rows
+            float *ws = p.parts + int64_t(slot * REP + copy) * (D + 2) * p.part_rows;
+            if (REP > 1 && whole) {
+                // the copies' sums added: each at the largest of their m, every copy a part of the
+                // rows (an item that is cut leaves the copies to the join, as parts of their own)
                 float f = 0.0f, all = 0.0f, big = -INFINITY;
                 float *own = reinterpret_cast<float *>(stage);
                 own[lane] = m;
@@ -860,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     if (k == copy) f = w;
                 }
                 if (!(ok = soft_sync())) break;
-                if (whole) f = all == 0.0f ? 0.0f : f / all;
+                f = all == 0.0f ? 0.0f : f / all;
 #pragma unroll
                 for (int j = 0; j < D; j += 32) {
                     if (warp_live) {
@@ -893,29 +898,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                                 v.z += u.z;
                                 v.w += u.w;
                             }
-                            if (whole) {
-                                const uint32_t ry = wk.mt * kRows + full_y, iy = ry / uint32_t(p.G);
-                                const int64_t o_row =
-                                    (int64_t(wk.r) * p.N + iy) * p.Hq + wk.h * p.G + (ry - iy * uint32_t(p.G));
-                                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + o_row * D + j + my_piece * 4) =
-                                    make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
-                            } else {
-                                *reinterpret_cast<float4 *>(ws + full_y * D + j + my_piece * 4) = v;
-                            }
+                            const uint32_t ry = wk.mt * kRows + full_y, iy = ry / uint32_t(p.G);
+                            const int64_t o_row =
+                                (int64_t(wk.r) * p.N + iy) * p.Hq + wk.h * p.G + (ry - iy * uint32_t(p.G));
+                            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + o_row * D + j + my_piece * 4) =
+                                make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
                         }
                     }
                     if (!(ok = soft_sync())) break;
                 }
                 if (!ok) break;
-                if (live && copy == 0) {
-                    if (!whole) {
-                        ws[D * p.part_rows + row] = big;
-                        ws[(D + 1) * p.part_rows + row] = all;
-                    } else if (p.lse) {
-                        p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
-                            all == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(all));
-                    }
-                }
+                if (live && copy == 0 && p.lse)
+                    p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
+                        all == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(all));
             } else if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 if (warp_live) {
@@ -970,10 +965,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         __syncwarp();
 #pragma unroll
                         for (int t = 0; t < 32; t += 4) {
-                            const int y = t + my_row;
-                            if (warp * 32 + y < rows)
-                                *reinterpret_cast<uint4 *>(ws + (warp * 32 + y) * D + j + my_piece * 4) =
-                                    *reinterpret_cast<const uint4 *>(stage + y * 128 + ((my_piece ^ (y & 7)) << 4));
+                            const int y = (warp % kQuads) * 32 + t + my_row;
+                            if (y < rows)
+                                *reinterpret_cast<uint4 *>(ws + y * D + j + my_piece * 4) =
+                                    *reinterpret_cast<const uint4 *>(stage + (t + my_row) * 128 +
+                                                                     ((my_piece ^ ((t + my_row) & 7)) << 4));
                         }
                         __syncwarp();
                     }
@@ -990,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     int64_t last = (end - 1) * ctas / total;
                     while (last + 1 < ctas && total * (last + 1) / ctas <= end - 1) ++last;
                     while (total * last / ctas > end - 1) --last;
-                    meta = Meta{wk.r, wk.h, wk.mt, int32_t(last), rows, 0, 0, 0};
+                    meta = Meta{wk.r, wk.h, wk.mt, int32_t(last), rows, 0, REP, 0};
                 }
             }
             tc_fence_before();                           // O is read before the next item's products (p_ready)
@@ -1009,29 +1005,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
     if (tid == 0 && hd.failed) p.meta[cta].failed = 1;
 }
 
-template <int D>
+template <int D, int ROWS>
 struct JoinSmem {
-    static constexpr int kMost = kMaxSms * Shape<D>::kCtas;          // parts at most
-    float weights[kJoinRows][kMost], parts[kJoinRows][kMost], big[kJoinRows], sum[kJoinRows];
-    float sums[kJoinWarps][kJoinRows][D];
+    static constexpr int kMost = kMaxSms * Shape<D>::kCtas;          // ranges at most, of up to 4 copies
+    float weights[ROWS][4 * kMost], big[ROWS], sum[ROWS];
+    float sums[kJoinWarps][ROWS][D];
     Meta metas[kMost];
 };
 
 // Joins the parts of the item that CTA c of attention_kernel began and did not end, the
 // rows of this CTA's blockIdx.y.  Few parts (many items, each cut once or twice): a warp
-// per row, the parts' maxima, sums and rows loaded together.  Many (few long items):
-// kJoinRows rows at a time, first their weights 2^(c (m_k - M)), a warp per row and a
-// lane per part; then each warp sums every eighth part over those rows, and the warps'
-// sums are added.
-template <typename T, int D>
-__device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> &sm) {
+// for two rows, the parts' maxima, sums and rows loaded together.  Many (few long items):
+// ROWS rows at a time, first their weights 2^(c (m_k - M)), a warp per row and a lane
+// per part; then each warp sums every eighth part over those rows, and the warps' sums
+// are added.
+template <typename T, int D, int ROWS>
+__device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D, ROWS> &sm) {
     constexpr int E = D / 32;                            // columns of a lane
-    constexpr int kFirst = D == 64 ? 4 : D == 128 ? 2 : 1;           // parts of a warp in flight
+    constexpr int kFirst = 512 / D / ROWS > 0 ? 512 / D / ROWS * (D == 256 ? 1 : 2) : 1;     // parts of a warp in flight
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t size = int64_t(D + 2) * p.part_rows;   // of a part
-    const int count = meta.last - c + 1;
-    const float *own = p.parts + int64_t(2 * c + 1) * size, *more = own + size;    // the first, then every second
-    auto part = [&](int k) { return k ? more + int64_t(2 * (k - 1)) * size : own; };
+    // the slot 2c + 1, then every second one after 2c + 2, each with its copies
+    const int copies = meta.copies, shift = copies == 4 ? 2 : copies == 2 ? 1 : 0;
+    const int count = (meta.last - c + 1) * copies;
+    auto part = [&](int k) {
+        const int range = k >> shift, slot = range ? 2 * (c + range) : 2 * c + 1;
+        return p.parts + int64_t((slot << shift) + (k & (copies - 1))) * size;
+    };
     auto place = [&](int row) {                          // the row's place in out / D and in lse
         const int rr = meta.mt * kRows + row, i = rr / p.G;
         return (int64_t(meta.r) * p.N + i) * p.Hq + meta.h * p.G + (rr - i * p.G);
@@ -1045,46 +1045,54 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> 
             p.lse[place(row)] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(sum));
     };
     if (count <= kFewParts) {
-        // a warp per row, the parts' maxima, sums and rows loaded together
-        for (int row = blockIdx.y * kJoinWarps + warp; row < meta.rows; row += gridDim.y * kJoinWarps) {
-            float m[kFewParts], s[kFewParts], o[E] = {};
-            float2 v[kFewParts][E / 2];
+        constexpr int kPair = D == 256 ? 1 : 2;          // rows at a time
+        const int step = gridDim.y * kJoinWarps;
+        for (int row0 = blockIdx.y * kJoinWarps + warp; row0 < meta.rows; row0 += kPair * step) {
+            float m[kPair][kFewParts], s[kPair][kFewParts];
+            float2 v[kPair][kFewParts][E / 2];
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k) {
-                const float *src = part(k < count ? k : 0);
-                m[k] = k < count ? src[D * p.part_rows + row] : -INFINITY;
-                s[k] = k < count ? src[(D + 1) * p.part_rows + row] : 0.0f;      // 0: the row sees nothing of the part
+            for (int y = 0; y < kPair; ++y)
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e)
-                    v[k][e] = reinterpret_cast<const float2 *>(src + row * D + lane * E)[e];
-            }
-            float big = -INFINITY, sum = 0.0f;
+                for (int k = 0; k < kFewParts; ++k) {
+                    const int row = min(row0 + y * step, meta.rows - 1);
+                    const float *src = part(k < count ? k : 0);
+                    m[y][k] = k < count ? src[D * p.part_rows + row] : -INFINITY;
+                    s[y][k] = k < count ? src[(D + 1) * p.part_rows + row] : 0.0f;   // 0: the row sees nothing of it
 #pragma unroll
-            for (int k = 0; k < kFewParts; ++k)
-                if (s[k] != 0.0f) big = fmaxf(big, m[k]);
-#pragma unroll
-            for (int k = 0; k < kFewParts; ++k) {
-                const float w = s[k] == 0.0f ? 0.0f : m[k] == big ? 1.0f : exp2f((m[k] - big) * p.c);
-                if (w == 0.0f) continue;
-                sum += w * s[k];
-#pragma unroll
-                for (int e = 0; e < E / 2; ++e) {
-                    o[2 * e] += w * v[k][e].x;
-                    o[2 * e + 1] += w * v[k][e].y;
+                    for (int e = 0; e < E / 2; ++e)
+                        v[y][k][e] = reinterpret_cast<const float2 *>(src + row * D + lane * E)[e];
                 }
+#pragma unroll
+            for (int y = 0; y < kPair; ++y) {
+                if (row0 + y * step >= meta.rows) break;
+                float big = -INFINITY, sum = 0.0f, o[E] = {};
+#pragma unroll
+                for (int k = 0; k < kFewParts; ++k)
+                    if (s[y][k] != 0.0f) big = fmaxf(big, m[y][k]);
+#pragma unroll
+                for (int k = 0; k < kFewParts; ++k) {
+                    const float w = s[y][k] == 0.0f ? 0.0f : m[y][k] == big ? 1.0f : exp2f((m[y][k] - big) * p.c);
+                    if (w == 0.0f) continue;
+                    sum += w * s[y][k];
+#pragma unroll
+                    for (int e = 0; e < E / 2; ++e) {
+                        o[2 * e] += w * v[y][k][e].x;
+                        o[2 * e + 1] += w * v[y][k][e].y;
+                    }
+                }
+                finish(row0 + y * step, o, big, sum);
             }
-            finish(row, o, big, sum);
         }
         return;
     }
-    for (int row0 = blockIdx.y * kJoinRows; row0 < meta.rows; row0 += gridDim.y * kJoinRows) {
-        const int rows = min(kJoinRows, meta.rows - row0);
+    for (int row0 = blockIdx.y * ROWS; row0 < meta.rows; row0 += gridDim.y * ROWS) {
+        const int rows = min(ROWS, meta.rows - row0);
         // the warp's first parts on their way while the weights are worked out
-        float2 v[kFirst][kJoinRows][E / 2];
-        auto fetch = [&](float2 (&to)[kJoinRows][E / 2], int k) {
+        float2 v[kFirst][ROWS][E / 2];
+        auto fetch = [&](float2 (&to)[ROWS][E / 2], int k) {
             const float2 *src = reinterpret_cast<const float2 *>(part(k) + row0 * D + lane * E);
 #pragma unroll
-            for (int y = 0; y < kJoinRows; ++y)
+            for (int y = 0; y < ROWS; ++y)
 #pragma unroll
                 for (int e = 0; e < E / 2; ++e)
                     to[y][e] = k < count && y < rows ? src[y * (D / 2) + e] : make_float2(0.0f, 0.0f);
@@ -1098,7 +1106,6 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> 
             for (int k = lane; k < count; k += 32) {
                 const float mk = part(k)[D * p.part_rows + row], sk = part(k)[(D + 1) * p.part_rows + row];
                 weight[k] = sk == 0.0f ? -INFINITY : mk;
-                sm.parts[warp][k] = sk;
                 if (sk != 0.0f) big = fmaxf(big, mk);
             }
 #pragma unroll
@@ -1107,7 +1114,7 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> 
                 const float mk = weight[k];
                 const float w = mk == -INFINITY ? 0.0f : exp2f((mk - big) * p.c);
                 weight[k] = w;
-                if (w != 0.0f) sum += w * sm.parts[warp][k];
+                if (w != 0.0f) sum += w * part(k)[(D + 1) * p.part_rows + row];
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -1117,14 +1124,14 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> 
             }
         }
         __syncthreads();
-        float o[kJoinRows][E] = {};
+        float o[ROWS][E] = {};
         for (int k = warp; k < count; k += kFirst * kJoinWarps) {
 #pragma unroll
             for (int f = 0; f < kFirst; ++f) {
                 const int at = k + f * kJoinWarps;
                 if (at >= count) break;
 #pragma unroll
-                for (int y = 0; y < kJoinRows; ++y) {
+                for (int y = 0; y < ROWS; ++y) {
                     const float w = y < rows ? sm.weights[y][at] : 0.0f;
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e) {
@@ -1138,7 +1145,7 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> 
         }
         // the warps' sums; then warp y adds and finishes row y
 #pragma unroll
-        for (int y = 0; y < kJoinRows; ++y)
+        for (int y = 0; y < ROWS; ++y)
 #pragma unroll
             for (int e = 0; e < E; ++e) sm.sums[warp][y][e * 32 + lane] = o[y][e];
         __syncthreads();
@@ -1156,9 +1163,9 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D> 
 
 // The items that were cut: CTA x takes those begun by CTAs x, x + gridDim.x, ... of
 // attention_kernel.  A wait that ran out anywhere makes the whole call's rows NaN.
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 4) join_kernel(const __grid_constant__ Params p) {
-    __shared__ JoinSmem<D> sm;
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 3) join_kernel(const __grid_constant__ Params p) {
+    __shared__ JoinSmem<D, ROWS> sm;
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     const int tid = threadIdx.x;
@@ -1178,7 +1185,7 @@ __global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 4) join_kernel(co
         return;
     }
     for (int c = blockIdx.x, k = 0; c < p.ctas; c += gridDim.x, ++k)
-        if (sm.metas[k].r >= 0) join_item<T, D>(p, c, sm.metas[k], sm);
+        if (sm.metas[k].r >= 0) join_item<T, D, ROWS>(p, c, sm.metas[k], sm);
 }
 
 // -------------------------------------------------------------------- host ----
@@ -1190,9 +1197,14 @@ int ctas_for(int D, int sms) { return sms * (D == 256 ? 1 : 2); }
 // Rows of a part: even, so that every part's rows are 16-byte aligned.
 int part_rows_for(int64_t N, int64_t G) { return int(N * G < kRows ? (N * G + 1) / 2 * 2 : kRows); }
 
+// Copies of the block's rows in a tile: those that fit a half or a quarter of it are
+// there twice or four times.
+int copies_for(int64_t N, int64_t G) { return N * G <= 32 ? 4 : N * G <= 64 ? 2 : 1; }
+
 size_t workspace_for(int32_t N, int32_t G, int32_t D) {
     const size_t ctas = size_t(ctas_for(D, kMaxSms));
-    return ctas * sizeof(Meta) + ctas * 2 * size_t(D + 2) * size_t(part_rows_for(N, G)) * sizeof(float);
+    return ctas * sizeof(Meta) +
+           ctas * 2 * size_t(copies_for(N, G)) * size_t(D + 2) * size_t(part_rows_for(N, G)) * sizeof(float);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1230,9 +1242,8 @@ int cache_map(EncodeTiled fn, CUtensorMap *map, const void *base, int32_t type, 
 template <typename T, int D>
 int launch(Params &p, cudaStream_t stream) {
     using S = Shape<D>;
-    // rows that fit a half or a quarter of the tile are there twice or four times
-    const int64_t rows = int64_t(p.N) * p.G;
-    auto kernel = rows <= 32 ? attention_kernel<T, D, 4> : rows <= 64 ? attention_kernel<T, D, 2> : attention_kernel<T, D, 1>;
+    const int copies = copies_for(p.N, p.G);
+    auto kernel = copies == 4 ? attention_kernel<T, D, 4> : copies == 2 ? attention_kernel<T, D, 2> : attention_kernel<T, D, 1>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "shared-memory opt-in");
     cudaLaunchAttribute attr[1];
@@ -1249,17 +1260,18 @@ int launch(Params &p, cudaStream_t stream) {
     if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
     lookup_note_launch();
     // The join.  With about as many items as ranges each is cut once or twice, and a few
-    // CTAs an item do; a few long items have tens of parts and take more, and where those
-    // CTAs times the ranges would be several waves of mostly idle ones, fewer CTAs share
-    // the ranges (an odd number: evenly cut items begin at even distances).
+    // CTAs an item do; a few long items have tens of parts and take more, a row each where
+    // there are few rows too.  Where those CTAs times the ranges would be several waves of
+    // mostly idle ones, fewer CTAs share the ranges (an odd number: evenly cut items begin
+    // at even distances).
     const int64_t items = int64_t(p.B) * p.Hkv * ((int64_t(p.N) * p.G + kRows - 1) / kRows);
-    const int most = (p.part_rows + kJoinRows - 1) / kJoinRows;
-    const int per = std::min(most, 3 * items >= p.ctas ? 4 : 16);
+    const bool single = items * p.part_rows < 512;
+    const int per = std::min(single ? p.part_rows : (p.part_rows + 3) / 4, 3 * items >= p.ctas ? 4 : 16);
     const int64_t over = int64_t(per) * p.ctas <= 1216 ? p.ctas : std::min<int64_t>(p.ctas, 2 * items + 1);
     cfg.gridDim = dim3(unsigned(over), per);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    r = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, p);
+    r = cudaLaunchKernelEx(&cfg, single ? join_kernel<T, D, 1> : join_kernel<T, D, 4>, p);
     if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
     lookup_note_launch();
     return LOOKUP_DRAFT_OK;
