@@ -65,8 +65,8 @@ struct CUstream_st;
  * For a pair (a, b) at position p: a' = a cos - b sin, b' = b cos + a sin, in
  * float32, rounded once; elements rot .. D and v are copied.  Scaling for long
  * contexts is a matter of the table's angles.
- * Errors: LOOKUP_DRAFT_EINVAL for sizes below their ranges, D > 1024, a page_size that is
- * not a power of two, one of k and v without the other or without a cache,
+ * Errors: LOOKUP_DRAFT_EINVAL for sizes below their ranges, D > 1024, B * N >= 2^31, a
+ * page_size that is not a power of two, one of k and v without the other or without a cache,
  * q without out_q, a null kv_len or block_table, or pointers not aligned to
  * their elements.
  */

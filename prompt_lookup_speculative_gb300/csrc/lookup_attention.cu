@@ -72,7 +72,7 @@ struct Shape {
     // waits, a dozen instructions of 40 ns); at D = 64 a tile of 64 positions has 16 KB,
     // for which that is too long (94 us where tiles of 128 take 7x us, ragged lengths).
     static constexpr int kTile = D == 64 ? 128 : 64;
-    static constexpr int kItemUnits = D == 64 ? 4 : 8;       // what an item's begin and end cost, in tiles
+    static constexpr int kItemUnits = D == 64 ? 8 : D == 128 ? 6 : 12;      // what an item's begin and end cost, in tiles
     // D = 64: K and V share a slot (a wait and a commit less), and one S tile is enough,
     // since P has tensor memory of its own: the next S comes as soon as this one is read.
     // Otherwise two S tiles, P over S, and slots for K and V apart, which fill earlier.

@@ -3,7 +3,7 @@
 // The contract is in include/lookup_target.h (lookup_kv_append).  What bounds it: the
 // bytes of q, k and v, read once and written once.  One launch: each thread takes one
 // unit of 16 elements of a head (for a rotated unit, the 8 pairs that share 8
-// angles) for up to kHeads heads of one token, so the angles are read once for them
+// angles) for kHeads heads of one token, so the angles are read once for them
 // and all their 16-byte loads are in flight together.  Sizes, strides or addresses
 // that are not multiples of 16 bytes take a kernel of one pair of elements per thread.
 // The last CTAs of either kernel report the requests with tokens that have no slot.
@@ -25,7 +25,7 @@ using lkd::launch_pdl;
 using lkd::wait_for_prerequisite_grid;
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 4;                // heads of a thread
+constexpr int kHeads = 2;                // heads of a thread (4 take more registers, and fewer threads fit)
 constexpr int kMaxD = 1024;
 
 struct Strides {
@@ -111,20 +111,21 @@ __device__ inline void turn(uint32_t &x, uint32_t &y, float c0, float s0, float 
 }
 
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) append_units_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 4) append_units_kernel(const __grid_constant__ Params p) {
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     if (int(blockIdx.x) >= p.grid) return report(p);
-    const int units = p.D / 16;
+    const uint32_t units = p.D / 16;
     const int q_groups = p.q ? (p.Hq + kHeads - 1) / kHeads : 0, k_groups = p.k ? (p.Hkv + kHeads - 1) / kHeads : 0;
-    const int groups = q_groups + 2 * k_groups;
-    const int64_t tok0 = int64_t(blockIdx.x) * p.tokens;
-    const int b0 = int(tok0 / p.N), i0 = int(tok0 - int64_t(b0) * p.N);
-    for (int x = threadIdx.x; x < p.tokens * units * groups; x += kThreads) {
-        const int t = x / (units * groups);
-        const int u = x % units;                         // neighbouring threads: neighbouring units of a head
-        int g = x / units - t * groups;
-        const int b = b0 + (i0 + t) / p.N, i = (i0 + t) % p.N;
+    const uint32_t per = units * (q_groups + 2 * k_groups);          // threads of a token
+    const uint32_t tok0 = blockIdx.x * uint32_t(p.tokens);
+    const int b0 = int(tok0 / uint32_t(p.N)), i0 = int(tok0 - uint32_t(b0) * uint32_t(p.N));
+    for (uint32_t x = threadIdx.x; x < p.tokens * per; x += kThreads) {
+        const uint32_t t = x / per, rest = x - t * per;
+        int g = int(rest / units);
+        const int u = int(rest - g * units);             // neighbouring threads: neighbouring units of a head
+        int b = b0, i = i0 + int(t);
+        for (; i >= p.N; i -= p.N) ++b;
         if (b >= p.B) return;
         const bool is_q = g < q_groups, is_k = !is_q && g < q_groups + k_groups;
         if (!is_q) g -= is_k ? q_groups : q_groups + k_groups;
@@ -266,6 +267,7 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
     if (rotary && (rot < 2 || rot > D || (rot & 1) || max_pos < 1)) return LOOKUP_DRAFT_EINVAL;
     if (type != LOOKUP_TYPE_F16 && type != LOOKUP_TYPE_BF16) return LOOKUP_DRAFT_EINVAL;
     if (B == 0 || N == 0) return LOOKUP_DRAFT_OK;
+    if (int64_t(B) * N > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
     if (!kv_len || !block_table || !k != !v || (k && (!k_cache || !v_cache || !k_strides || !v_strides)) ||
         (q && (!out_q || !q_strides)))
         return LOOKUP_DRAFT_EINVAL;
@@ -302,7 +304,6 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
             grid = (int64_t(B) * N + p.tokens - 1) / p.tokens;
         } else {
             const int64_t heads = (q ? int64_t(Hq) : 0) + (k ? 2 * int64_t(Hkv) : 0);
-            if (int64_t(B) * N > (int64_t(1) << 40) / heads) return LOOKUP_DRAFT_EINVAL;
             grid = (int64_t(B) * N * heads * ((D + 1) / 2) + kThreads - 1) / kThreads;
         }
     }
