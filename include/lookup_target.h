@@ -124,7 +124,9 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
  *
  * block         int32 [B][P] (0 <= P <= 65536), len int32 [B], as for lookup_verify
  *               (a len outside [0, P] gives the error row accepted = -1,
- *               ncommit = 0, commit all -1, logprobs all 0)
+ *               ncommit = 0, commit all -1, logprobs all 0; so do all requests of a
+ *               call whose bounded waits run out on the device,
+ *               lookup_draft_set_wait_limit_ns)
  * logits        type (f32, f16 or bf16) [B][P + 1][V]: the target's logits at each
  *               position given the block before it; the last axis dense, the
  *               request and position strides in elements.  A NaN counts as -infinity.

@@ -251,6 +251,35 @@ __device__ inline bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+__device__ inline void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ inline bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Waits for phase `parity` of the barrier, at most `limit` clocks and only while no
+// other wait of the CTA has run out (*failed, in shared memory); false otherwise.
+__device__ inline bool wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t from = clock64();
+    for (;;) {
+        if (*failed) return false;
+        if (uint64_t(clock64()) - from > limit) {
+            *failed = 1;
+            return false;
+        }
+        if (mbar_try_wait(bar, parity)) return true;
+    }
+}
+
 __device__ inline uint64_t global_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));

@@ -48,9 +48,11 @@
 namespace {
 
 using lkd::allow_dependent_launch;
+using lkd::mbar_arrive;
 using lkd::mbar_expect_tx;
 using lkd::mbar_init;
 using lkd::mbar_try_wait;
+using lkd::wait;
 using lkd::smem_addr;
 using lkd::wait_for_prerequisite_grid;
 
@@ -328,10 +330,6 @@ __device__ inline void tma_load(uint32_t dst, const CUtensorMap *map, int32_t x,
         : "memory");
 }
 
-__device__ inline void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 __device__ inline void copy16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -365,31 +363,6 @@ struct Head {
     int64_t warp_sum[kThreads / 32];
 };
 static_assert(sizeof(Head) <= kBarBytes, "Head fits ahead of the tiles");
-
-__device__ inline bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// Waits for phase `parity` of the barrier, at most `limit` clocks and only while no
-// other wait of the CTA has run out; false otherwise.
-__device__ inline bool wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t from = clock64();
-    for (;;) {
-        if (*failed) return false;
-        if (uint64_t(clock64()) - from > limit) {
-            *failed = 1;
-            return false;
-        }
-        if (mbar_try_wait(bar, parity)) return true;
-    }
-}
 
 // The same for a whole warp: every lane waits, and all go on or none does.
 __device__ inline bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit) {

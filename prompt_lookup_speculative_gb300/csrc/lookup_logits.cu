@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -32,15 +33,17 @@ using lkd::kMaxBlock;
 using lkd::launch_pdl;
 using lkd::wait_for_prerequisite_grid;
 
-constexpr int kStatThreads = 256;
-constexpr int kUnroll = 8;               // 16-byte loads in flight per thread
+constexpr int kStatWarps = 16;           // of a CTA of stats_kernel, each with a ring of its own
+constexpr int kStatThreads = 32 * kStatWarps;
+constexpr int kPer = 8;                  // 16-byte pieces of a lane and tile
+constexpr int kTile = 32 * kPer;         // pieces of a tile: 4 KB, one bulk copy
+constexpr int kRing = 3;                 // tiles in flight per warp: 192 KB per SM
+constexpr int kSegTiles = 8;             // tiles of a segment at most
+constexpr int kMaxCtas = 160;            // CTAs of stats_kernel at most, one per SM
 constexpr int kPickThreads = 512;
 constexpr int kKept = 32;                // positions whose statistics a CTA of pick_kernel keeps
 constexpr int kMaxCluster = 8;           // CTAs per request in pick_kernel at most
 constexpr int kRace = 16;                // logits in flight per thread there
-constexpr int kMaxSegs = 64;             // segments of a row at most
-constexpr int kSegBytes = 4 * kUnroll * kStatThreads * 16;  // of a segment at most: four passes (where kMaxSegs allows)
-constexpr int kSegMin = 8192;            // logits of a segment at least, where there is a choice
 constexpr int kMaxV = 1 << 30;
 
 struct Params {
@@ -54,6 +57,9 @@ struct Params {
     int32_t *out_accepted, *out_commit, *out_ncommit;
     float *out_logprobs;
     float4 *part;                        // [B][P + 1][segs]: m, s, index of m (bits), unused
+    int32_t *status;                     // [ctas]: not 0 where a wait of stats_kernel ran out
+    int32_t ctas;
+    uint64_t limit;                      // clocks that a wait may take
 };
 
 __device__ inline float to_f32(float x) { return x; }
@@ -167,137 +173,190 @@ __device__ inline float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-__device__ inline float2 mul2(float2 a, float2 b) {
+__device__ inline float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
         : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
 
-// One segment of one row per CTA.  The row is taken in aligned pieces of 16 bytes
-// (the first and the last may be part of the row only), kUnroll of them per thread
-// and pass, all in flight together; the SM's other CTAs compute meanwhile.  Per pass
-// the maximum first, in the type itself, then one factor for the sum so far, then the
-// weights as 2^((x - m) log2(e) / T): the difference before the product, because a
-// product m log2(e) / T, rounded, would shift every weight of the row by up to 3e-6.
+struct StatSmem {
+    uint64_t full[kStatWarps][kRing];
+    uint32_t next, failed;
+};
+
+// Every row that a proposal is tested in, once.  One CTA per SM; its warps take one of the
+// CTA's segments after another (every ctas-th of all of them), each on its own: a warp
+// streams its segment by bulk copies through a ring of three tiles, so that 192 KB per SM
+// are in flight however far the warps have come, and nothing waits for a neighbour.
+// (CTAs of 256 threads that load a segment into registers and then compute took 52 us
+// for 233 MB of bf16 logits, and a ring shared by the CTA's warps 60 us: there each
+// tile's chain of wait, maximum, weights and sum was on everyone's path.)  A row is taken
+// in aligned pieces of 16 bytes; the first and the last may be part of the row only, and
+// lanes add those logits by themselves.  Per tile the maximum first, in the type itself,
+// then one factor for the sum so far, then the weights as 2^(x c - m c), c = log2(e) /
+// T, one fused operation each.  The product m c is rounded first, which shifts all
+// weights by one factor of up to 1 + 3e-6: the sum is brought back by it.
 template <typename T>
-__global__ void __launch_bounds__(kStatThreads, sizeof(T) == 4 ? 4 : 3) stats_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kStatThreads, 1) stats_kernel(const __grid_constant__ Params p) {
     constexpr int E = 16 / int(sizeof(T));               // logits of a piece
-    __shared__ Stat warp_stat[kStatThreads / 32];
+    extern __shared__ __align__(128) uint4 rings[];      // [kStatWarps][kRing][kTile]
+    __shared__ StatSmem sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile uint32_t *failed = &sm.failed;
+    uint4 *ring = rings + warp * kRing * kTile;
+    if (tid == 0) {
+        sm.next = 0;
+        sm.failed = 0;
+    }
+    if (lane == 0) {
+        for (int k = 0; k < kRing; ++k) lkd::mbar_init(lkd::smem_addr(&sm.full[warp][k]), 1);
+        lkd::fence_barrier_init();
+    }
+    __syncthreads();
     wait_for_prerequisite_grid();
     allow_dependent_launch();
-    const uint32_t row_id = blockIdx.x / uint32_t(p.segs);
-    const int seg = int(blockIdx.x - row_id * uint32_t(p.segs));
-    const int b = int(row_id / uint32_t(p.P + 1)), i = int(row_id - uint32_t(b) * uint32_t(p.P + 1));
-    const int n = p.len[b];
-    if (i > n || n > p.P) return;                       // a row no proposal is tested in
-    const T *row = static_cast<const T *>(p.logits) + b * p.lb + i * p.lp;
-    const bool greedy = is_greedy(p, b);
-    const float inv_t = inv_temperature(p, b);
-    const float c = inv_t * 1.4426950408889634f;
-    const int mis = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));   // logits before the row in piece 0
-    const int pieces = (p.V + mis + E - 1) / E;
-    const int per = int((uint32_t(pieces) + uint32_t(p.segs) - 1) / uint32_t(p.segs));
-    const int lo = min(seg * per, pieces), hi = min(lo + per, pieces);
-    const int whole0 = mis ? 1 : 0, whole1 = (p.V + mis) / E;         // pieces [whole0, whole1) are all the row's
-    const uint4 *base = reinterpret_cast<const uint4 *>(row - mis);
+    const uint32_t units = uint32_t(p.B) * uint32_t(p.P + 1) * uint32_t(p.segs);
     const uint32_t none = std::is_same<T, float>::value ? 0xff800000u
                           : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
-
-    Stat v{-INFINITY, 0.0f, INT32_MAX};
-    for (int k0 = lo + int(threadIdx.x); k0 < hi; k0 += kUnroll * kStatThreads) {
-        uint4 r[kUnroll];
-        if (k0 >= whole0 && k0 + (kUnroll - 1) * kStatThreads < min(hi, whole1)) {
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) r[k] = __ldcs(base + k0 + k * kStatThreads);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                const int at = k0 + k * kStatThreads;
-                r[k] = make_uint4(none, none, none, none);
-                if (at < hi && at >= whole0 && at < whole1) {
-                    r[k] = __ldcs(base + at);
-                } else if (at < hi) {                    // a piece that is part of the row only
-                    uint32_t w[4] = {none, none, none, none};
-                    for (int e = 0; e < E; ++e) {
-                        const int j = at * E + e - mis;
-                        if (j < 0 || j >= p.V) continue;
-                        if (sizeof(T) == 4) {
-                            w[e % 4] = reinterpret_cast<const uint32_t *>(row)[j];
-                        } else {
-                            const uint32_t x = reinterpret_cast<const uint16_t *>(row)[j];
-                            w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | (x << 16) : (w[e / 2] & 0xffff0000u) | x;
-                        }
+    int at = 0;                                          // the ring's next tile to use, and its parity
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok) {
+        uint32_t u = 0;
+        if (lane == 0) u = atomicAdd(&sm.next, 1u);
+        u = blockIdx.x + __shfl_sync(0xffffffffu, u, 0) * uint32_t(p.ctas);
+        if (u >= units) break;
+        const uint32_t row_id = u / uint32_t(p.segs);
+        const int seg = int(u - row_id * uint32_t(p.segs));
+        const int b = int(row_id / uint32_t(p.P + 1)), i = int(row_id - uint32_t(b) * uint32_t(p.P + 1));
+        const int n = p.len[b];
+        if (i > n || n > p.P) continue;                 // a row no proposal is tested in
+        const T *row = static_cast<const T *>(p.logits) + b * p.lb + i * p.lp;
+        const int mis = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));    // logits before the row in piece 0
+        const int pieces = (p.V + mis + E - 1) / E;
+        const int per = int((uint32_t(pieces) + uint32_t(p.segs) - 1) / uint32_t(p.segs));
+        const int lo = min(seg * per, pieces), hi = min(lo + per, pieces);
+        // pieces [first, last) are all the row's: the ones that bulk copies bring
+        const int first = max(lo, mis ? 1 : 0), last = max(min(hi, (p.V + mis) / E), first);
+        const int tiles = (last - first + kTile - 1) / kTile;
+        const uint4 *base = reinterpret_cast<const uint4 *>(row - mis) + first;
+        auto fetch = [&](int t, int to) {                // by one lane: tile t into place `to`
+            const uint32_t bytes = uint32_t(min(kTile, last - first - t * kTile)) * 16;
+            const uint32_t bar = lkd::smem_addr(&sm.full[warp][to]);
+            lkd::mbar_expect_tx(bar, bytes);
+            lkd::bulk_copy_g2s_stream(lkd::smem_addr(ring + to * kTile), base + t * kTile, bytes, bar);
+        };
+        if (lane == 0)
+            for (int t = 0; t < min(tiles, kRing); ++t) fetch(t, (at + t) % kRing);
+        const bool greedy = is_greedy(p, b);
+        const float inv_t = inv_temperature(p, b), c = inv_t * 1.4426950408889634f;
+        Stat v{-INFINITY, 0.0f, INT32_MAX};
+        // the row's first and last logits, short of a piece: a lane each, at most 2 (E - 1)
+        {
+            const int head = mis ? min(E - mis, p.V) : 0, tail = max((p.V + mis) / E * E - mis, head);
+            const int j = lane < E ? lane : tail + lane - E;
+            const bool mine = lane < E ? lo == 0 && lane < head : hi == pieces && lo < hi && lane < 2 * E && j < p.V;
+            const float x = mine ? logit(row, j) : -INFINITY;
+            if (x > -INFINITY) v = Stat{x, 1.0f, j};
+        }
+        for (int t = 0; ok && t < tiles; ++t) {
+            ok = __all_sync(0xffffffffu, lkd::wait(lkd::smem_addr(&sm.full[warp][at]), phase, failed, p.limit));
+            if (!ok) {                                   // no copy outlives the CTA
+                for (int k = 0; k < min(tiles - t, kRing); ++k) {
+                    const uint64_t until = lkd::global_ns() + 1000000000ull;
+                    while (!lkd::mbar_try_wait(lkd::smem_addr(&sm.full[warp][at]), phase) && lkd::global_ns() < until) {
                     }
-                    r[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (++at == kRing) {
+                        at = 0;
+                        phase ^= 1;
+                    }
                 }
+                break;
             }
-        }
-        uint4 top = r[0];
+            const int count = min(kTile, last - first - t * kTile);
+            uint4 r[kPer];
 #pragma unroll
-        for (int k = 1; k < kUnroll; ++k) top = max_words(top, r[k], T());
-        float big = -INFINITY;
+            for (int k = 0; k < kPer; ++k) r[k] = ring[at * kTile + k * 32 + lane];
+            __syncwarp();
+            if (lane == 0 && t + kRing < tiles) fetch(t + kRing, at);
+            if (++at == kRing) {
+                at = 0;
+                phase ^= 1;
+            }
+            if (count < kTile) {                         // (past the copy the ring holds older logits)
 #pragma unroll
-        for (int w = 0; w < E / 2; ++w) {
-            const float2 x = two(top, w, T());
-            big = fmaxf(big, fmaxf(x.x, x.y));
-        }
-        if (big > v.m) {
-            v.s = v.m == -INFINITY ? 0.0f : v.s * weight(v.m, big, inv_t);
-            v.m = big;
-            if (greedy) {
+                for (int k = 0; k < kPer; ++k)
+                    if (k * 32 + lane >= count) r[k] = make_uint4(none, none, none, none);
+            }
+            uint4 top = r[0];
 #pragma unroll
-                for (int k = kUnroll - 1; k >= 0; --k)
+            for (int k = 1; k < kPer; ++k) top = max_words(top, r[k], T());
+            float big = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < E / 2; ++w) {
+                const float2 x = two(top, w, T());
+                big = fmaxf(big, fmaxf(x.x, x.y));
+            }
+            if (big > v.m) {
+                v.s = v.m == -INFINITY ? 0.0f : v.s * weight(v.m, big, inv_t);
+                v.m = big;
+                v.at = INT32_MAX;
+            }
+            if (greedy && big == v.m) {                  // the lowest index so far of the lane's maximum
+#pragma unroll
+                for (int k = kPer - 1; k >= 0; --k)
 #pragma unroll
                     for (int w = E / 2 - 1; w >= 0; --w) {
                         const float2 x = two(r[k], w, T());
-                        const int j = (k0 + k * kStatThreads) * E + 2 * w - mis;
-                        if (x.y == big) v.at = j + 1;
-                        if (x.x == big) v.at = j;
+                        const int j = (first + t * kTile + k * 32 + lane) * E + 2 * w - mis;
+                        if (x.y == big) v.at = min(v.at, j + 1);
+                        if (x.x == big) v.at = min(v.at, j);
                     }
             }
-        }
-        float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
-        const float2 minus_m = make_float2(-v.m, -v.m), cc = make_float2(c, c);
+            const float mc = v.m * c;
+            float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+            const float2 cc = make_float2(c, c), minus = make_float2(-mc, -mc);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-#pragma unroll
-            for (int w = 0; w < E / 2; ++w) {
-                const float2 a = mul2(add2(two(r[k], w, T()), minus_m), cc);
-                const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
-                if (w & 1) s1 = add2(s1, e);
-                else s0 = add2(s0, e);
-            }
-        float sum = (s0.x + s0.y) + (s1.x + s1.y);
-        if (!(sum <= FLT_MAX)) {                         // infinities or NaN among them: one by one
-            sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
+            for (int k = 0; k < kPer; ++k)
 #pragma unroll
                 for (int w = 0; w < E / 2; ++w) {
-                    const float2 x = two(r[k], w, T());
-                    if (x.x > -INFINITY) sum += weight(x.x, v.m, inv_t);
-                    if (x.y > -INFINITY) sum += weight(x.y, v.m, inv_t);
+                    const float2 a = fma2(two(r[k], w, T()), cc, minus);
+                    const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+                    if (w & 1) s1 = add2(s1, e);
+                    else s0 = add2(s0, e);
                 }
+            float sum = (s0.x + s0.y) + (s1.x + s1.y);
+            // mc is m c rounded, off by err: every weight is 2^err too large, so the sum is
+            const float err = fmaf(v.m, c, -mc);
+            sum = fmaf(sum, err * -0.6931471805599453f, sum);
+            if (!(sum <= FLT_MAX)) {                     // infinities or NaN among them: one by one
+                sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k)
+#pragma unroll
+                    for (int w = 0; w < E / 2; ++w) {
+                        const float2 x = two(r[k], w, T());
+                        if (x.x > -INFINITY) sum += weight(x.x, v.m, inv_t);
+                        if (x.y > -INFINITY) sum += weight(x.y, v.m, inv_t);
+                    }
+            }
+            v.s += sum;
         }
-        v.s += sum;
+        const Stat all = warp_join(v, inv_t, greedy);
+        if (lane == 0 && ok) p.part[u] = make_float4(all.m, all.s, __int_as_float(all.at), 0.0f);
     }
-    v = warp_join(v, inv_t, greedy);
-    if ((threadIdx.x & 31) == 0) warp_stat[threadIdx.x >> 5] = v;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        v = threadIdx.x < kStatThreads / 32 ? warp_stat[threadIdx.x] : Stat{-INFINITY, 0.0f, INT32_MAX};
-        v = warp_join(v, inv_t, greedy);
-        if (threadIdx.x == 0) p.part[int64_t(row_id) * p.segs + seg] = make_float4(v.m, v.s, __int_as_float(v.at), 0.0f);
-    }
+    if (tid == 0) p.status[blockIdx.x] = int32_t(sm.failed);
 }
 
 // Row (b, i)'s statistics from its segments, by one warp (every lane gets them).
 __device__ inline Stat row_stat(const Params &p, int b, int i, float inv_t, int lane) {
     const float4 *part = p.part + (int64_t(b) * (p.P + 1) + i) * p.segs;
     Stat v{-INFINITY, 0.0f, INT32_MAX};
+#pragma unroll 4
     for (int k = lane; k < p.segs; k += 32) {
         const float4 q = part[k];
         v = join(v, Stat{q.x, q.y, __float_as_int(q.z)}, inv_t);
@@ -383,7 +442,10 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     const int P = p.P, n = p.len[b];
     int32_t *commit = p.out_commit + int64_t(b) * (P + 1);
     float *lps = p.out_logprobs ? p.out_logprobs + int64_t(b) * (P + 1) : nullptr;
-    if (n < 0 || n > P) {                               // no valid block: an error row
+    // no valid block, or logits that did not arrive in time: an error row
+    bool bad = tid < p.ctas && p.status[tid] != 0;
+    static_assert(kMaxCtas <= kPickThreads, "a thread per CTA of stats_kernel");
+    if (__syncthreads_or(bad || n < 0 || n > P)) {
         if (rank) return;
         for (int i = tid; i <= P; i += kPickThreads) {
             commit[i] = -1;
@@ -513,15 +575,12 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     }
 }
 
-// Segments of a row of `size`-byte logits: enough CTAs for two waves of stats_kernel
-// where rows are few, at most kSegBytes each.
-int segments(int32_t B, int32_t P, int32_t V, int size) {
-    const int64_t rows = int64_t(B) * (P + 1);
-    const int64_t want = 152 * 8 / (rows > 0 ? rows : 1) + 1;
-    const int64_t least = (int64_t(V) * size + kSegBytes - 1) / kSegBytes, most = (int64_t(V) + kSegMin - 1) / kSegMin;
-    int64_t s = want < most ? want : most;
-    s = s > least ? s : least;
-    return int(s > kMaxSegs ? kMaxSegs : s);
+// Segments of a row of `size`-byte logits: a tile each while there are fewer tiles than
+// warps, kSegTiles tiles at most.
+int64_t segments(int32_t B, int32_t P, int32_t V, int size) {
+    const int64_t tiles = (int64_t(V) * size / 16 + 2 + kTile - 1) / kTile;          // of a row
+    const int64_t each = std::min<int64_t>(std::max<int64_t>(tiles * B * (P + 1) / (152 * kStatWarps), 1), kSegTiles);
+    return (tiles + each - 1) / each;
 }
 
 // CTAs of a request's cluster: a power of two, one per 4096 logits of its race as
@@ -534,7 +593,10 @@ int cluster_for(int32_t B, int32_t V) {
 
 template <typename T>
 int launch(const Params &p, cudaStream_t stream) {
-    int rc = launch_pdl(stats_kernel<T>, unsigned(int64_t(p.B) * (p.P + 1) * p.segs), unsigned(kStatThreads), stream, p);
+    constexpr size_t kBytes = size_t(kStatWarps) * kRing * kTile * 16;
+    const cudaError_t opt = cudaFuncSetAttribute(stats_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kBytes));
+    if (opt != cudaSuccess) return lookup_record_cuda_error(opt, "shared-memory opt-in");
+    int rc = launch_pdl(stats_kernel<T>, unsigned(p.ctas), unsigned(kStatThreads), stream, p, kBytes);
     if (rc != LOOKUP_DRAFT_OK) return rc;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -562,7 +624,8 @@ extern "C" {
 
 size_t lookup_verify_logits_workspace_bytes(int32_t B, int32_t P, int32_t V) {
     if (B < 0 || P < 0 || P > kMaxBlock || V < 1 || V >= kMaxV) return 0;
-    return size_t(B) * size_t(P + 1) * size_t(segments(B, P, V, 4)) * sizeof(float4) + 16;
+    return size_t(B) * size_t(P + 1) * size_t(std::max(segments(B, P, V, 4), segments(B, P, V, 2))) * sizeof(float4) +
+           kMaxCtas * sizeof(int32_t);
 }
 
 int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *logits, const int64_t *logits_strides,
@@ -574,8 +637,8 @@ int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *l
     if (B < 0 || P < 0 || P > kMaxBlock || V < 1 || V >= kMaxV) return LOOKUP_DRAFT_EINVAL;
     if (type != LOOKUP_TYPE_F32 && type != LOOKUP_TYPE_F16 && type != LOOKUP_TYPE_BF16) return LOOKUP_DRAFT_EINVAL;
     if (B == 0) return LOOKUP_DRAFT_OK;
-    const int segs = segments(B, P, V, type == LOOKUP_TYPE_F32 ? 4 : 2);
-    if (int64_t(B) * (P + 1) * segs > INT32_MAX || int64_t(B) * kMaxCluster > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
+    const int64_t segs = segments(B, P, V, type == LOOKUP_TYPE_F32 ? 4 : 2);
+    if (segs > INT32_MAX / (int64_t(B) * (P + 1)) || int64_t(B) * kMaxCluster > INT32_MAX) return LOOKUP_DRAFT_EINVAL;
     if ((P > 0 && !block) || !len || !logits || !logits_strides || !out_accepted || !out_commit || !out_ncommit ||
         !workspace)
         return LOOKUP_DRAFT_EINVAL;
@@ -590,9 +653,20 @@ int lookup_verify_logits(const int32_t *block, const int32_t *len, const void *l
         if (misaligned(q, 4)) return LOOKUP_DRAFT_EINVAL;
     if (workspace_bytes < lookup_verify_logits_workspace_bytes(B, P, V)) return LOOKUP_DRAFT_EINVAL;
     const bool with_q = noise && qprobs && P > 0;
-    Params p{block, len, logits, logits_strides[0], logits_strides[1], noise, noise ? temperature : nullptr, u,
-             with_q ? qprobs : nullptr, with_q ? qprobs_strides[0] : 0, with_q ? qprobs_strides[1] : 0, point_mass,
-             B, P, V, segs, cluster_for(B, V), out_accepted, out_commit, out_ncommit, out_logprobs, static_cast<float4 *>(workspace)};
+    int sms = 0;
+    const int rc = lkd::sm_count(&sms);
+    if (rc != LOOKUP_DRAFT_OK) return rc;
+    Params p{};
+    p.block = block, p.len = len, p.logits = logits, p.lb = logits_strides[0], p.lp = logits_strides[1];
+    p.noise = noise, p.temperature = noise ? temperature : nullptr, p.u = u, p.qprobs = with_q ? qprobs : nullptr;
+    if (with_q) p.qb = qprobs_strides[0], p.qp = qprobs_strides[1];
+    p.point_mass = point_mass, p.B = B, p.P = P, p.V = V, p.segs = int32_t(segs), p.cluster = cluster_for(B, V);
+    p.out_accepted = out_accepted, p.out_commit = out_commit, p.out_ncommit = out_ncommit, p.out_logprobs = out_logprobs;
+    const int64_t units = int64_t(B) * (P + 1) * segs;
+    p.ctas = int32_t(std::min<int64_t>(units, std::min(sms, kMaxCtas)));
+    p.part = static_cast<float4 *>(workspace);
+    p.status = reinterpret_cast<int32_t *>(p.part + units);
+    p.limit = 2 * lookup_wait_limit_ns();                // at 2 GHz
     if (type == LOOKUP_TYPE_F32) return launch<float>(p, stream);
     if (type == LOOKUP_TYPE_F16) return launch<__half>(p, stream);
     return launch<__nv_bfloat16>(p, stream);

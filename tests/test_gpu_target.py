@@ -427,6 +427,22 @@ def test_verify_frequencies_follow_the_target():
         assert chi < 35, (chi, seen.tolist(), (B * p).tolist())
 
 
+def test_verify_waits_that_run_out_give_error_rows():
+    """A wait limit of a nanosecond: every request reports it, and the next call is right."""
+    c = verify_case(5, 3, 32000, BF16, "point", 12)
+    d = {k: None if v is None else v.cuda() for k, v in c.items()}
+    pkg.set_wait_limit_ns(1)
+    try:
+        acc, commit, nc, lps = pkg.lookup_verify_logits(d["block"], d["length"], d["logits"], noise=d["noise"], u=d["u"],
+                                                        temperature=d["temperature"])
+        torch.cuda.synchronize()
+    finally:
+        pkg.set_wait_limit_ns(0)
+    assert acc.tolist() == [-1] * 5 and nc.tolist() == [0] * 5
+    assert bool((commit == -1).all()) and bool((lps == 0).all())
+    check_verify(c, least=0.6)
+
+
 # ------------------------------------------------- streams, graphs, launches ----
 def test_calls_on_another_stream_and_in_a_graph():
     a = attention_case([40, 150], [4, 4], 4, 4, 2, 128, 16, BF16, 31)
