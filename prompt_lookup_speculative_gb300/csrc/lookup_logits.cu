@@ -38,7 +38,7 @@ constexpr int kStatThreads = 32 * kStatWarps;
 constexpr int kPer = 8;                  // 16-byte pieces of a lane and tile
 constexpr int kTile = 32 * kPer;         // pieces of a tile: 4 KB, one bulk copy
 constexpr int kRing = 3;                 // tiles in flight per warp: 192 KB per SM
-constexpr int kSegTiles = 8;             // tiles of a segment at most
+constexpr int kSegTiles = 4;            // tiles of a segment at most (with 8 the last round is longer: 58 us for 56)
 constexpr int kMaxCtas = 160;            // CTAs of stats_kernel at most, one per SM
 constexpr int kPickThreads = 512;
 constexpr int kKept = 32;                // positions whose statistics a CTA of pick_kernel keeps
