@@ -239,7 +239,7 @@ def _check(rc: int, lib) -> None:
 def _stream_handle(stream) -> int:
     import torch
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream)
 
 
@@ -936,58 +936,37 @@ class ContextCache:
 
 
 # ------------------------------------------- the target's side of a verify step ----
-_TYPES = {"torch.float32": 0, "torch.float16": 1, "torch.bfloat16": 2}      # LOOKUP_TYPE_* of include/lookup_target.h
-_Strides = {n: ctypes.c_int64 * n for n in (2, 3)}
+_target_module = None
 
 
-def _type_code(t, name, least=0):
-    code = _TYPES.get(str(t.dtype), -1)
-    if code < least:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return code
+def _target():
+    """The compiled entry of these calls (csrc/target_binding.cpp): it checks the tensors,
+    allocates what is not given and enters the library, in a fraction of the time that
+    takes from Python, which for these kernels would be longer than they run."""
+    global _target_module
+    if _target_module is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries are what the module links against)
+        lib = load_library()
+        with _lib_lock:
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"the compiled binding {path} is missing; run build() first")
+            spec = importlib.util.spec_from_file_location("_target", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.entry_points(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+                "lookup_kv_append", "lookup_paged_attention", "lookup_paged_attention_workspace_bytes",
+                "lookup_verify_logits", "lookup_verify_logits_workspace_bytes")))
+            _target_module = module
+    return _target_module
 
 
-def _strided(t, shape, dtype, device, name):
-    """Check a device tensor whose last axis is dense and whose other strides are free;
-    return its pointer and the C array of those strides."""
-    if t.dtype != dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}: the last axis must be dense")
-    return t.data_ptr(), _Strides[len(shape) - 1](*st[:-1])
-
-
-def _cuda_device(t, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
-
-
-def _call(fn, dev, stream, *args):
-    """Run an entry point on the device, its stream last."""
-    import torch
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_handle(stream))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream_handle(stream))
-    if rc:
-        raise LookupDraftError(rc, load_library())
-
-
-def _scratch(nbytes, workspace, device, stream):
-    """The call's workspace: the caller's, or one from PyTorch's allocator that stays
-    reserved until the stream is past the call."""
-    import torch
-    if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        return workspace, workspace.numel() * workspace.element_size()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws, nbytes
+def _outputs_or_error(out):
+    if type(out) is int:
+        raise LookupDraftError(out, load_library())
+    return out
 
 
 def rotary_table(max_pos: int, rot: int, base: float = 10000.0, scaling=None, device=None):
@@ -1040,56 +1019,14 @@ def rotary_table(max_pos: int, rot: int, base: float = 10000.0, scaling=None, de
     return table.to(torch.float32).to(device if device is not None else "cuda").contiguous()
 
 
-def _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, dtype, dev):
-    """Check the paged cache's tensors; returns (pages, Hkv, page_size, max_pages, pointers)."""
-    import torch
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("k_cache must be [pages, Hkv, page_size, D] and block_table [B, max_pages]")
-    pages, hkv, page, _ = k_cache.shape
-    mp = block_table.shape[1]
-    shape = (pages, hkv, page, D)
-    ptrs = (_dev(k_cache, dtype, shape, dev, "k_cache"), _dev(v_cache, dtype, shape, dev, "v_cache"),
-            _dev(block_table, torch.int32, (B, mp), dev, "block_table"),
-            _dev(kv_len, torch.int32, (B,), dev, "kv_len"), _dev(q_len, torch.int32, (B,), dev, "q_len", optional=True))
-    return pages, hkv, page, mp, ptrs
-
-
 def lookup_kv_append(q, k, v, kv_len, block_table, k_cache, v_cache, rotary=None, q_len=None,
                      interleaved: bool = False, out_q=None, status=None, stream=None):
     """Rotate a verify block's queries and keys and write its keys and values to the paged
     cache [pages, Hkv, page_size, D] (include/lookup_target.h).  q [B, N, Hq, D], k and
     v [B, N, Hkv, D] may be strided views; ``rotary`` is rotary_table's [max_pos, rot].
     Returns (rotated q [B, N, Hq, D], status [B]: 1 where a token had no slot)."""
-    import torch
-    lib = _lib or load_library()
-    dev = _cuda_device(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, N, Hq, D]")
-    B, N, hq, D = q.shape
-    dtype, code = q.dtype, _type_code(q, "q", 1)
-    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, dtype, dev)
-    qp, qs = _strided(q, (B, N, hq, D), dtype, dev, "q")
-    kp, ks = _strided(k, (B, N, hkv, D), dtype, dev, "k")
-    vp, vs = _strided(v, (B, N, hkv, D), dtype, dev, "v")
-    rp, max_pos, rot = None, 0, 0
-    if rotary is not None:
-        if rotary.dim() != 2:
-            raise ValueError("rotary must be [max_pos, rot]")
-        max_pos, rot = rotary.shape
-        rp = _dev(rotary, torch.float32, (max_pos, rot), dev, "rotary")
-    if out_q is None:
-        out_q = torch.empty((B, N, hq, D), dtype=dtype, device=dev)
-    else:
-        _dev(out_q, dtype, (B, N, hq, D), dev, "out_q")
-    if status is None:
-        status = torch.empty(B, dtype=torch.int32, device=dev)
-    else:
-        _dev(status, torch.int32, (B,), dev, "status")
-    if N == 0:
-        status.zero_()
-    _call(lib.lookup_kv_append, dev, stream, qp, qs, kp, ks, vp, vs, kl, ql, bt, B, N, hq, hkv, D, mp, pages, page, rp,
-          rot, max_pos, 1 if interleaved else 0, code, kc, vc, out_q.data_ptr(), status.data_ptr())
-    return out_q, status
+    return _outputs_or_error((_target_module or _target()).kv_append(
+        q, k, v, kv_len, block_table, k_cache, v_cache, rotary, q_len, interleaved, out_q, status, stream))
 
 
 def lookup_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None, scale=None, window: int = 0,
@@ -1098,27 +1035,8 @@ def lookup_paged_attention(q, k_cache, v_cache, block_table, kv_len, q_len=None,
     (include/lookup_target.h): q [B, N, Hq, D], token i of request r at position
     kv_len[r] + i.  ``scale`` defaults to D**-0.5; ``window`` > 0 limits each token to
     itself and the window - 1 before it.  Returns (out [B, N, Hq, D], lse float32 [B, N, Hq])."""
-    import torch
-    lib = _lib or load_library()
-    dev = _cuda_device(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, N, Hq, D]")
-    B, N, hq, D = q.shape
-    dtype, code = q.dtype, _type_code(q, "q", 1)
-    pages, hkv, page, mp, (kc, vc, bt, kl, ql) = _paged(k_cache, v_cache, block_table, kv_len, q_len, B, D, dtype, dev)
-    qp, qs = _strided(q, (B, N, hq, D), dtype, dev, "q")
-    if out is None:
-        out = torch.empty((B, N, hq, D), dtype=dtype, device=dev)
-    else:
-        _dev(out, dtype, (B, N, hq, D), dev, "out")
-    if lse is None:
-        lse = torch.empty((B, N, hq), dtype=torch.float32, device=dev)
-    else:
-        _dev(lse, torch.float32, (B, N, hq), dev, "lse")
-    ws, nbytes = _scratch(lib.lookup_paged_attention_workspace_bytes(B, N, hq, hkv, D), workspace, dev, stream)
-    _call(lib.lookup_paged_attention, dev, stream, qp, qs, kc, vc, bt, kl, ql, B, N, hq, hkv, D, mp, pages, page,
-          D ** -0.5 if scale is None else scale, window, code, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), nbytes)
-    return out, lse
+    return _outputs_or_error((_target_module or _target()).attention(
+        q, k_cache, v_cache, block_table, kv_len, q_len, scale, window, out, lse, workspace, stream))
 
 
 def lookup_verify_logits(block, length, logits, noise=None, u=None, temperature=None, qprobs=None, point_mass=None,
@@ -1129,32 +1047,9 @@ def lookup_verify_logits(block, length, logits, noise=None, u=None, temperature=
     ``u`` [B, P], per-request ``temperature`` (0 = greedy) and the proposal
     distributions ``qprobs`` [B, P, V] (None = point masses).  Returns (accepted [B],
     commit [B, P + 1], ncommit [B], logprobs float32 [B, P + 1])."""
-    import torch
-    lib = _lib or load_library()
-    dev = _cuda_device(logits, "logits")
-    if block.dim() != 2 or logits.dim() != 3:
-        raise ValueError("block must be [B, P] and logits [B, P + 1, V]")
-    B, P = block.shape
-    V = logits.shape[2]
-    i32, f32 = torch.int32, torch.float32
-    code = _type_code(logits, "logits")
-    lp, ls = _strided(logits, (B, P + 1, V), logits.dtype, dev, "logits")
-    qp, qs = (None, None) if qprobs is None else _strided(qprobs, (B, P, V), f32, dev, "qprobs")
-    if out is None:
-        out = (torch.empty(B, dtype=i32, device=dev), torch.empty((B, P + 1), dtype=i32, device=dev),
-               torch.empty(B, dtype=i32, device=dev), torch.empty((B, P + 1), dtype=f32, device=dev))
-    else:
-        for t, dtype, shape, name in zip(out, (i32, i32, i32, f32), ((B,), (B, P + 1), (B,), (B, P + 1)),
-                                         ("accepted", "commit", "ncommit", "logprobs"), strict=True):
-            _dev(t, dtype, shape, dev, name)
-    acc, commit, nc, lps = out
-    ws, nbytes = _scratch(lib.lookup_verify_logits_workspace_bytes(B, P, V), workspace, dev, stream)
-    _call(lib.lookup_verify_logits, dev, stream, _dev(block, i32, (B, P), dev, "block"),
-          _dev(length, i32, (B,), dev, "len"), lp, ls, code, V, _dev(noise, f32, (B, V), dev, "noise", True),
-          _dev(temperature, f32, (B,), dev, "temperature", True), _dev(u, f32, (B, P), dev, "u", noise is None), qp, qs,
-          _dev(point_mass, i32, (B, P), dev, "point_mass", True), B, P, acc.data_ptr(), commit.data_ptr(), nc.data_ptr(),
-          lps.data_ptr(), ws.data_ptr(), nbytes)
-    return acc, commit, nc, lps
+    acc, commit, nc, lps = out if out is not None else (None, None, None, None)
+    return _outputs_or_error((_target_module or _target()).verify(
+        block, length, logits, noise, u, temperature, qprobs, point_mass, acc, commit, nc, lps, workspace, stream))
 
 
 class PagedKVCache:

@@ -12,12 +12,19 @@ also compiled with LOOKUP_DRAFT_CHECKED=1 into ``_build/liblookup_draft_checked.
 the same entry points with device-side index checks (include/lookup_draft.h).  The CUDA runtime is linked
 statically, so the library loads on a machine without a GPU (its calls then
 fail with a CUDA error) and needs nothing from the Python environment.
+
+``csrc/target_binding.cpp``, the Python entry of the target's operators, is compiled
+with the host compiler against the installed PyTorch's headers (its version is part
+of the file's name) and does not link against the library.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -36,6 +43,8 @@ LIB_PATH = os.path.join(BUILD_DIR, "liblookup_draft.so")
 # index checks that set bits in a check word instead of faulting.
 CHECKED_SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("lookup_draft.cu", "read_floor.cu")]
 CHECKED_LIB_PATH = os.path.join(BUILD_DIR, "liblookup_draft_checked.so")
+
+BINDING_SOURCE = os.path.join(PKG_DIR, "csrc", "target_binding.cpp")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -60,19 +69,39 @@ def compile_command(out: str, extra: list[str] | None = None, checked: bool = Fa
             "-I", INCLUDE_DIR, *defines, "-o", out, *sources, *(extra or [])]
 
 
+def binding_path() -> str | None:
+    """Where the target operators' Python entry is built; None without PyTorch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    return os.path.join(BUILD_DIR, f"_target-{importlib.metadata.version('torch')}.so")
+
+
+def binding_command(out: str) -> list[str]:
+    """Host compiler's command line of the Python entry of the target's operators."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+            "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+            "-I", os.path.join(cuda, "include"), "-I", INCLUDE_DIR, "-o", out, BINDING_SOURCE,
+            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def up_to_date() -> bool:
-    for lib in (LIB_PATH, CHECKED_LIB_PATH):
+    for lib in (LIB_PATH, CHECKED_LIB_PATH, binding_path()):
+        if lib is None:
+            continue
         if not os.path.exists(lib):
             return False
         t = os.path.getmtime(lib)
-        if not all(os.path.getmtime(p) <= t for p in SOURCES + HEADERS + [__file__]):
+        if not all(os.path.getmtime(p) <= t for p in SOURCES + HEADERS + [BINDING_SOURCE, __file__]):
             return False
     return True
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build both libraries (regular and checked, compiled side by side) if either
-    is missing or stale; return the regular library's path."""
+    """Build both libraries (regular and checked) and the target operators' Python
+    entry, side by side, if one is missing or stale; return the regular library's path."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -81,6 +110,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for lib, checked in ((LIB_PATH, False), (CHECKED_LIB_PATH, True)):
         tmp = lib + f".tmp{os.getpid()}"
         jobs.append((subprocess.Popen(compile_command(tmp, extra, checked)), tmp, lib))
+    if binding_path():
+        tmp = binding_path() + f".tmp{os.getpid()}"
+        jobs.append((subprocess.Popen(binding_command(tmp)), tmp, binding_path()))
     failed = [p.args for p, _, _ in jobs if p.wait() != 0]
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])

@@ -266,9 +266,11 @@ __device__ inline bool mbar_test(uint32_t bar, uint32_t parity) {
 }
 
 // Waits for phase `parity` of the barrier, at most `limit` clocks and only while no
-// other wait of the CTA has run out (*failed, in shared memory); false otherwise.
+// other wait of the CTA has run out (*failed, in shared memory); false otherwise.  A
+// limit of two clocks or less (a nanosecond) has run out before the first look, so
+// that setting it shows what a wait that runs out leads to, every time.
 __device__ inline bool wait(uint32_t bar, uint32_t parity, volatile uint32_t *failed, uint64_t limit) {
-    if (mbar_test(bar, parity)) return true;
+    if (limit > 2 && mbar_test(bar, parity)) return true;
     const uint64_t from = clock64();
     for (;;) {
         if (*failed) return false;

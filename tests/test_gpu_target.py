@@ -493,6 +493,52 @@ def test_cache_class_and_empty_calls():
     assert got[1].shape == (0, 4)
 
 
+def test_verify_step_example_follows_the_model():
+    """examples/verify_step.py, greedy and sampled: every greedily committed token has a
+    logit within 0.25 of the largest at its place, in a plain pass over the whole
+    sequence (each 16-bit rounding of the hidden row moves a logit by 2.8 * 2^-8 / sqrt
+    3 in the mean, five of them and the logits' own come to 0.03, eight times that is
+    0.25), and more than one token a step is committed in the mean."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "verify_step.py")
+    spec = importlib.util.spec_from_file_location("verify_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    V, steps = 64, 40
+    model = ex.Model(V, hq=4, hkv=2, d=64, max_pos=2048)
+    hist = ex.histories(5, V, 3)
+    got = ex.generate(model, hist, steps, 7)
+    assert sum(map(len, got)) > 1.2 * steps * len(hist)
+    emb, qkv, wo, head = (w.float() for w in (model.embed, model.qkv, model.out, model.head))
+    rot = model.rotary.float()
+    for h, g in zip(hist, got):
+        seq = torch.tensor(h + g, device="cuda")
+        L = seq.shape[0]
+        x = emb[seq]
+        q, k, v = (x @ qkv).view(L, 8, 64).split([4, 2, 2], 1)
+        cos, sin = rot[:L, None, :32], rot[:L, None, 32:]
+
+        def turn(z):
+            a, b = z[..., :32], z[..., 32:]
+            return torch.cat([a * cos - b * sin, b * cos + a * sin], -1)
+
+        q, k, v = turn(q), turn(k).repeat_interleave(2, 1), v.repeat_interleave(2, 1)
+        s = torch.einsum("ihd,jhd->hij", q, k) / 8.0
+        s.masked_fill_(torch.ones((L, L), dtype=torch.bool, device="cuda").triu(1), -math.inf)
+        a = torch.einsum("hij,jhd->ihd", s.softmax(-1), v)
+        z = (x + a.reshape(L, -1) @ wo) @ head
+        at = torch.arange(len(h) - 1, L - 1, device="cuda")
+        gap = z[at].amax(-1) - z[at, seq[at + 1]]
+        assert float(gap.max()) < 0.25
+    rng = torch.Generator(device="cuda")
+    rng.manual_seed(2)
+    sampled = ex.generate(model, hist, 5, 7, lambda B, K: dict(
+        u=torch.rand((B, K), device="cuda", generator=rng),
+        noise=torch.empty((B, V), device="cuda").exponential_(generator=rng)))
+    assert all(len(s) >= 5 and all(0 <= t < V for t in s) for s in sampled)
+
+
 def test_append_writes_past_32_bits():
     """A pool of more than 2^32 bytes: the last page's rows are where they belong."""
     pages, page, D = 70000, 64, 256                      # 2.3 GB each for k and v: 1.1e9 elements
