@@ -797,7 +797,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     if (!kTwice) tc_st(to, w);
                     tc_wait_st();
                 } else if (S::kOwnP) {
+                    // an idle warp keeps step with the others: with one P tile, it would otherwise
+                    // say that the next P is ready while this one is being written
                     mbar_arrive(smem_addr(&hd.s_free));
+                    if (it > 0 && !warp_wait(smem_addr(&hd.pv_done[before.at]), before.phase, failed, p.limit)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 tc_fence_before();
                 mbar_arrive(smem_addr(&hd.p_ready[buf]));

@@ -205,6 +205,31 @@ def test_attention_long_context_split(page, D):
     check_attention(*attention_case([5000, 17], [4, 4], 4, 4, 2, D, page, F16, 4))
 
 
+def filled_case(lens, qn, N, Hq, Hkv, D, page, dt, seed, spread=2.0):
+    """As attention_case, drawn as a whole: only slots past a request's end hold NaN."""
+    g = gen(seed)
+    table, pages = tables([n + c for n, c in zip(lens, qn)], page, g, spare=1)
+    kc, vc = (torch.randn((pages, Hkv, page, D), generator=g).to(dt) for _ in range(2))
+    for r, (n, c) in enumerate(zip(lens, qn)):
+        if (n + c) % page:
+            last = int(table[r, (n + c) // page])
+            kc[last, :, (n + c) % page:] = math.nan
+            vc[last, :, (n + c) % page:] = math.nan
+    q = (torch.randn((len(lens), N, Hq, D), generator=g) * spread).to(dt)
+    return q, kc, vc, table, torch.tensor(lens, dtype=torch.int32), torch.tensor(qn, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("D,N,Hq,Hkv,page,window", [
+    (64, 1, 8, 4, 16, 0), (64, 9, 16, 4, 32, 0), (64, 12, 32, 4, 64, 0), (64, 9, 16, 4, 128, 700), (64, 17, 32, 4, 64, 0),
+    (128, 1, 8, 4, 16, 0), (128, 9, 16, 4, 32, 0), (128, 12, 32, 4, 64, 300), (256, 5, 8, 4, 64, 0), (256, 12, 32, 4, 16, 0)])
+def test_attention_of_many_tiles_per_range(D, N, Hq, Hkv, page, window):
+    """Enough work that every range holds several tiles, begins and ends of items; blocks
+    from one token to N, so that some warps of a tile have no rows."""
+    lens = [1500 + (r * 977) % 1700 for r in range(14)] + [3, 127]
+    qn = [1 + (r * 5) % N for r in range(16)]
+    check_attention(*filled_case(lens, qn, N, Hq, Hkv, D, page, BF16, D + N), window=window)
+
+
 def test_attention_many_requests_of_mixed_length():
     g = gen(9)
     lens = torch.randint(0, 90, (700,), generator=g).tolist()
