@@ -13,8 +13,10 @@
 // Hq / Hkv query heads of one key-value head share every key they read, so their
 // N * G rows form the M = 128 rows of tcgen05 products (16 tokens of 8 heads fill
 // them exactly; fewer rows leave lanes idle, which costs no bytes): S = Q K^T of 128
-// rows by 64 positions into tensor memory, softmax by one thread per row, P back
-// into tensor memory over S, O += P V from there.
+// rows by a tile of 64 or 128 positions into tensor memory, softmax by one thread per
+// row, P back into tensor memory, O += P V from there.  P is rounded to the cache's type,
+// as the product's operand has to be (relative 2^-9 or 2^-12, the rounding of an output);
+// the sum takes the weights before that, and S, O, m and the sum are float32.
 //
 // Few rows: the tile has idle rows, and only the warps of the live ones have a softmax
 // to do, one SM quarter per 32 rows.  So a block of at most 64 (32) rows is in the tile
@@ -24,7 +26,7 @@
 // copies' sums are added at the end.
 //
 // Split: the work of all requests, heads and row tiles is laid end to end in units
-// of 64 positions and cut into equal contiguous ranges, one per CTA (two CTAs per
+// of a tile and cut into equal contiguous ranges, one per CTA (two CTAs per
 // SM), so that neither ragged lengths nor few requests leave an SM without work.
 // A CTA finds its range from kv_len and q_len on the device.  An item that lies in
 // one range is finished there; the parts of one that is cut go to the workspace and
@@ -61,7 +63,7 @@ constexpr int kSoftWarps = 4;            // one thread per row
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kThreads = 192;
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;       // of a CTA of join_kernel
-constexpr int kFewParts = 4;             // parts that a warp joins by itself
+constexpr int kFewParts = 4;             // parts that a warp joins by itself (1: 512 items of 48 rows 270 us, not 260)
 constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
 constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
 constexpr int kBarBytes = 1024;          // barriers and small state ahead of the tiles
@@ -72,9 +74,13 @@ struct Shape {
     static constexpr int kCtas = D == 256 ? 1 : 2;           // per SM
     // Positions of a tile.  The thread that issues the products takes 0.8 us a tile (four
     // waits, a dozen instructions of 40 ns); at D = 64 a tile of 64 positions has 16 KB,
-    // for which that is too long (94 us where tiles of 128 take 7x us, ragged lengths).
+    // for which that is too long (16 requests of 512 to 262144 positions, blocks of 8, 14
+    // heads on 2: 98 us, and 87 in tiles of 128).  At D = 128 and 256 64 positions have 32
+    // and 64 KB, and 128 would leave less than two tiles of K and V in a CTA's memory.
     static constexpr int kTile = D == 64 ? 128 : 64;
-    static constexpr int kItemUnits = D == 64 ? 8 : D == 128 ? 6 : 12;      // what an item's begin and end cost, in tiles
+    // What an item's begin and end cost, in tiles (counted as one tile: the same requests
+    // 101 us for 87, 2048 items of 1 to 2048 positions at D = 128 164 us for 139).
+    static constexpr int kItemUnits = D == 64 ? 8 : D == 128 ? 6 : 12;
     // D = 64: K and V share a slot (a wait and a commit less), and one S tile is enough,
     // since P has tensor memory of its own: the next S comes as soon as this one is read.
     // Otherwise two S tiles, P over S, and slots for K and V apart, which fill earlier.
@@ -1176,8 +1182,8 @@ int ctas_for(int D, int sms) { return sms * (D == 256 ? 1 : 2); }
 // Rows of a part: even, so that every part's rows are 16-byte aligned.
 int part_rows_for(int64_t N, int64_t G) { return int(N * G < kRows ? (N * G + 1) / 2 * 2 : kRows); }
 
-// Copies of the block's rows in a tile: those that fit a half or a quarter of it are
-// there twice or four times.
+// Copies of the block's rows in a tile at most: those that fit a half or a quarter of it
+// are there twice or four times.
 int copies_for(int64_t N, int64_t G) { return N * G <= 32 ? 4 : N * G <= 64 ? 2 : 1; }
 
 size_t workspace_for(int32_t N, int32_t G, int32_t D) {
@@ -1221,7 +1227,13 @@ int cache_map(EncodeTiled fn, CUtensorMap *map, const void *base, int32_t type, 
 template <typename T, int D>
 int launch(Params &p, cudaStream_t stream) {
     using S = Shape<D>;
-    const int copies = copies_for(p.N, p.G);
+    // Every copy of an item that is cut is a part of its own.  A few long items are cut into
+    // tens of parts, and half as many are faster than a softmax over a quarter of the
+    // columns: 8 items of 4096 positions at D = 128 take 16.0 us with two copies and 17.9
+    // with four, 2 of 30000 at D = 64 28 and 35.  With more items four are: 16 of 3000
+    // positions 15.4 and 15.9 us, 2048 of 1 to 2048 138 us and 156 (and 175 with one copy).
+    const int64_t items = int64_t(p.B) * p.Hkv * ((int64_t(p.N) * p.G + kRows - 1) / kRows);
+    const int copies = std::min(copies_for(p.N, p.G), items < 16 ? 2 : 4);
     auto kernel = copies == 4 ? attention_kernel<T, D, 4> : copies == 2 ? attention_kernel<T, D, 2> : attention_kernel<T, D, 1>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "shared-memory opt-in");
@@ -1239,11 +1251,12 @@ int launch(Params &p, cudaStream_t stream) {
     if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
     lookup_note_launch();
     // The join.  With about as many items as ranges each is cut once or twice, and a few
-    // CTAs an item do; a few long items have tens of parts and take more, a row each where
-    // there are few rows too.  Where those CTAs times the ranges would be several waves of
-    // mostly idle ones, fewer CTAs share the ranges (an odd number: evenly cut items begin
-    // at even distances).
-    const int64_t items = int64_t(p.B) * p.Hkv * ((int64_t(p.N) * p.G + kRows - 1) / kRows);
+    // CTAs an item do; a few long items have tens of parts and take 16 (32 items of 56 rows
+    // at D = 64: the whole call 87 us, and 108 with 4).  A CTA takes four rows at a time; one
+    // where all items together have few rows (8 items of 4: 17.9 us, and 19.4 by fours; 4 of
+    // 128: 45 us by fours, and 67).  Where those CTAs times the ranges would be several waves
+    // of mostly idle ones, fewer CTAs share the ranges (those 32 items: 87 us, and 91 with a
+    // CTA for each range; an odd number: evenly cut items begin at even distances).
     const bool single = items * p.part_rows < 512;
     const int per = std::min(single ? p.part_rows : (p.part_rows + 3) / 4, 3 * items >= p.ctas ? 4 : 16);
     const int64_t over = int64_t(per) * p.ctas <= 1216 ? p.ctas : std::min<int64_t>(p.ctas, 2 * items + 1);
