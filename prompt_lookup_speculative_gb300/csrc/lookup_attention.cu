@@ -32,6 +32,11 @@
 // one range is finished there; the parts of one that is cut go to the workspace and
 // join_kernel adds them, in the order of the ranges: no atomics, the same bits every
 // time.
+//
+// Short items: what runs once per item, at its begin and end, waits for its instructions
+// more than for anything else, so that code is kept small: loops there are rolled, one
+// copy of each step.  The next item's Q and first page ids are loaded during an item.
+// 2048 items of 1 to 2048 positions, 4 heads each at D = 128: 138 us before, 87 after.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
@@ -80,7 +85,7 @@ struct Shape {
     static constexpr int kTile = D == 64 ? 128 : 64;
     // What an item's begin and end cost, in tiles (counted as one tile: the same requests
     // 101 us for 87, 2048 items of 1 to 2048 positions at D = 128 164 us for 139).
-    static constexpr int kItemUnits = D == 64 ? 8 : D == 128 ? 6 : 12;
+    static constexpr int kItemUnits = D == 64 ? 8 : D == 128 ? 4 : 6;
     // D = 64: K and V share a slot (a wait and a commit less), and one S tile is enough,
     // since P has tensor memory of its own: the next S comes as soon as this one is read.
     // Otherwise two S tiles, P over S, and slots for K and V apart, which fill earlier.
@@ -122,22 +127,22 @@ struct Params {
 // Request r's part of the work: tokens of the block, positions its rows see, tiles.
 struct Request {
     int32_t n, kv;
-    int64_t lo, end;                     // some row sees positions [lo, end)
+    int32_t lo, end;                     // some row sees positions [lo, end)
     int32_t t0, nt, mts;                 // first tile, tiles, row tiles
 };
 
 template <typename S>
-__device__ inline Request request_of(const Params &p, int r) {
+__device__ __noinline__ Request request_of(const Params &p, int r) {
     Request q;
     q.n = p.q_len ? min(max(p.q_len[r], 0), p.N) : p.N;
     q.kv = max(p.kv_len[r], 0);
-    q.end = min(int64_t(q.kv) + q.n, int64_t(p.max_pages) << p.page_shift);
-    q.lo = p.window > 0 ? max(int64_t(q.kv) - p.window + 1, int64_t(0)) : 0;
+    q.end = int32_t(min(int64_t(q.kv) + q.n, int64_t(p.max_pages) << p.page_shift));     // at most 2^31 - 129
+    q.lo = p.window > 0 ? max(q.kv - p.window + 1, 0) : 0;
     if (q.n == 0 || q.end <= q.lo) {
         q.t0 = q.nt = 0;
     } else {
-        q.t0 = int32_t(q.lo / S::kTile);
-        q.nt = int32_t((q.end + S::kTile - 1) / S::kTile) - q.t0;
+        q.t0 = q.lo / S::kTile;
+        q.nt = (q.end + S::kTile - 1) / S::kTile - q.t0;
     }
     q.mts = (q.n * p.G + kRows - 1) / kRows;
     return q;
@@ -497,20 +502,22 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         uint32_t n = 0;                                  // slots filled so far
         Place<S::kSlots> to{0, 0};                       // the next one
         bool ok = true;
-        for (; ok && wk.valid(); wk.next(p)) {
-            const int32_t *table = p.table + int64_t(wk.r) * p.max_pages;
-            auto entry = [&](int64_t at) { return at < p.max_pages ? table[at] : -1; };
-            // page ids, 32 at a time, and the next 32 ahead of their use
-            const int64_t x_first = int64_t(wk.q.t0 + wk.a) * kTile;
-            int64_t base = x_first >> p.page_shift;
-            int32_t cur = entry(base + lane), nxt = entry(base + 32 + lane);
+        // page ids, 32 at a time, and the next 32 ahead of their use; the first of an item
+        // are on their way during the item before
+        auto entry = [&](int32_t r, int64_t at) { return at < p.max_pages ? p.table[int64_t(r) * p.max_pages + at] : -1; };
+        auto first_page = [&](const Walk<S> &w) { return (int64_t(w.q.t0 + w.a) * kTile) >> p.page_shift; };
+        Walk<S> ahead = wk;
+        int32_t ids = wk.valid() ? entry(wk.r, first_page(wk) + lane) : -1;
+        for (; ok && wk.valid(); wk = ahead) {
+            int64_t base = first_page(wk);
+            int32_t cur = ids, nxt = entry(wk.r, base + 32 + lane);
             for (int t = wk.a; ok && t < wk.b; ++t) {
                 const int64_t x0 = int64_t(wk.q.t0 + t) * kTile;
                 int64_t at = x0 >> p.page_shift;
                 if (at - base >= 32) {                   // a tile's pages never straddle a window: 32 % per_tile == 0
                     base += 32;
                     cur = nxt;
-                    nxt = entry(base + 32 + lane);
+                    nxt = entry(wk.r, base + 32 + lane);
                 }
                 const int32_t page = __shfl_sync(0xffffffffu, cur, int(at - base) + my_page);
                 const int64_t x = x0 + my_page * box_rows;
@@ -533,6 +540,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         tma_load(dst, part ? &p.v_map : &p.k_map, my_col * 64, y, full(s));
                         if (S::kPair) tma_load(dst + S::kTileBytes, &p.v_map, my_col * 64, y, full(s));
                     }
+                }
+                if (t == wk.a) {
+                    ahead.next(p);
+                    if (ahead.valid()) ids = entry(ahead.r, first_page(ahead) + lane);
                 }
             }
         }
@@ -584,27 +595,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             };
             for (; ok && wk.valid(); wk.next(p), ++item) {
                 ok = wait(smem_addr(&hd.q_ready), item & 1, failed, p.limit);
-                for (int t = wk.a; ok && t < wk.b; ++t) {
-                    // K is there, and the S of kBufs tiles ago has been read; where P lies over S,
-                    // its product is over too
-                    ok = wait(full(k_at.at), k_at.phase, failed, p.limit) &&
-                         (!used || wait(S::kOwnP ? smem_addr(&hd.s_free) : smem_addr(&hd.pv_done[s_at.at]),
-                                        s_at.phase ^ 1, failed, p.limit));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t lo = k_lo + k_at.at * kSlotStep, d = tmem + s_at.at * kTile;
+                for (int t = wk.a; ok && t < wk.b + S::kAhead; ++t) {
+                    if (t < wk.b) {
+                        // K is there, and the S of kBufs tiles ago has been read; where P lies over S,
+                        // its product is over too
+                        ok = wait(full(k_at.at), k_at.phase, failed, p.limit) &&
+                             (!used || wait(S::kOwnP ? smem_addr(&hd.s_free) : smem_addr(&hd.pv_done[s_at.at]),
+                                            s_at.phase ^ 1, failed, p.limit));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t lo = k_lo + k_at.at * kSlotStep, d = tmem + s_at.at * kTile;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        tc_mma_ss(d, desc(q_hi, q_lo + (j / 4) * (kRows * 8) + (j % 4) * 2),
-                                  desc(k_hi, lo + (j / 4) * (kTile * 8) + (j % 4) * 2), kQk, j > 0);
-                    if (!S::kPair) tc_commit(empty(k_at.at));
-                    tc_commit(smem_addr(&hd.s_full[s_at.at]));
-                    k_at.step(S::kPair ? 1 : 2);
-                    s_at.step(1);
-                    used = used || s_at.phase;
-                    if (t - wk.a >= S::kAhead) pv(t - S::kAhead == wk.a);
+                        for (int j = 0; j < D / 16; ++j)
+                            tc_mma_ss(d, desc(q_hi, q_lo + (j / 4) * (kRows * 8) + (j % 4) * 2),
+                                      desc(k_hi, lo + (j / 4) * (kTile * 8) + (j % 4) * 2), kQk, j > 0);
+                        if (!S::kPair) tc_commit(empty(k_at.at));
+                        tc_commit(smem_addr(&hd.s_full[s_at.at]));
+                        k_at.step(S::kPair ? 1 : 2);
+                        s_at.step(1);
+                        used = used || s_at.phase;
+                    }
+                    if (ok && t - wk.a >= S::kAhead) pv(t - S::kAhead == wk.a);
                 }
-                for (int left = min(S::kAhead, wk.b - wk.a); ok && left > 0; --left) pv(wk.b - left == wk.a);
             }
             {                                            // nor does a product
                 tc_commit(smem_addr(&hd.drain));
@@ -631,48 +643,85 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
         unsigned char *stage = smem + kBarBytes + warp * 4096;       // 32 rows of 128 bytes, in Q's place
         Meta meta{-1, 0, 0, 0, 0, 0, 0, 0};
         bool ok = true;
-        for (; count > 0 && ok && wk.valid(); wk.next(p), ++item) {
+        // Q: a thread's pieces of 16 bytes.  Where they are few, the next item's are on their
+        // way during this one; otherwise, and where registers are short (two copies at D = 64:
+        // 80 us without, 83 with), they go from global to shared memory by themselves.
+        constexpr int kCh = D / 8, kStep = kRows / kCh;  // pieces of a row, rows of a pass
+        constexpr int kLoads = kRows / REP / kStep;
+        constexpr bool kEarly = kLoads <= 4 && !(D == 64 && REP == 2);
+        const int ch = thread % kCh;
+        auto q_piece = [&](const Walk<S> &w, int y) {
+            const uint32_t ry = w.mt * kRows + y, iy = ry / uint32_t(p.G);
+            return static_cast<const T *>(p.q) + w.r * p.qb + w.h * p.G * p.qh + ch * 8 + iy * p.qn +
+                   (ry - iy * p.G) * p.qh;
+        };
+        uint4 early[kEarly ? kLoads : 1];
+        auto load_q = [&](const Walk<S> &w) {
+            const int rows = min(kRows, w.q.n * p.G - w.mt * kRows);
+#pragma unroll
+            for (int k = 0; k < (kEarly ? kLoads : 0); ++k) {
+                const int y = thread / kCh + k * kStep;
+                if (y < rows) early[k] = *reinterpret_cast<const uint4 *>(q_piece(w, y));
+            }
+        };
+        Walk<S> ahead = wk;
+        auto advance = [&]() {
+            if (kEarly) wk = ahead;
+            else wk.next(p);
+        };
+        if (count > 0 && wk.valid()) load_q(wk);
+        for (; count > 0 && ok && wk.valid(); advance(), ++item) {
             const Request &q = wk.q;
             const int rows = min(kRows, q.n * p.G - wk.mt * kRows);
             const int rr = wk.mt * kRows + row;          // row of the request: token, then head of the group
             const bool live = row < rows;
             const int i = live ? rr / p.G : 0;
             const int head = wk.h * p.G + (live ? rr - i * p.G : 0);
-            // Q, 16 bytes at a time, where the products' swizzle wants it, all copies in
-            // flight together (idle rows keep what was there: a row of S depends on its own
-            // row of Q only).  Before it, the last item's result has left these bytes.
+            // Q where the products' swizzle wants it (idle rows keep what was there: a row of S
+            // depends on its own row of Q only).  Before it, the last item's result has left
+            // these bytes.
             if (item > 0 && !warp_wait(smem_addr(&hd.staged), (item - 1) & 1, failed, p.limit)) {
                 ok = false;
                 break;
             }
             {
-                constexpr int kCh = D / 8, kStep = kRows / kCh;          // chunks of a row, rows of a pass
-                const int ch = thread % kCh;
-                const T *src = static_cast<const T *>(p.q) + wk.r * p.qb + wk.h * p.G * p.qh + ch * 8;
+                const uint32_t flip = p.negate ? 0x80008000u : 0u;
                 unsigned char *dst = smem + kBarBytes + (ch >> 3) * (kRows * 128);
-                for (int y = thread / kCh; y < rows; y += kStep) {
-                    const uint32_t ry = wk.mt * kRows + y, iy = ry / uint32_t(p.G);
+                auto at = [&](int y, int k) { return dst + (y + k * kQuads * 32) * 128 + (((ch & 7) ^ (y & 7)) << 4); };
+                if (kEarly) {
 #pragma unroll
-                    for (int k = 0; k < REP; ++k)
-                        copy16(smem_addr(dst + (y + k * kQuads * 32) * 128 + (((ch & 7) ^ (y & 7)) << 4)),
-                               src + iy * p.qn + (ry - iy * p.G) * p.qh);
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                if (p.negate)
+                    for (int k = 0; k < kLoads; ++k) {
+                        const int y = thread / kCh + k * kStep;
+                        const uint4 v = early[k];
+                        if (y < rows)
+#pragma unroll
+                            for (int c = 0; c < REP; ++c)
+                                *reinterpret_cast<uint4 *>(at(y, c)) =
+                                    make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+                    }
+                } else {
                     for (int y = thread / kCh; y < rows; y += kStep)
 #pragma unroll
-                        for (int k = 0; k < REP; ++k) {
-                            uint4 *v = reinterpret_cast<uint4 *>(dst + (y + k * kQuads * 32) * 128 +
-                                                                 (((ch & 7) ^ (y & 7)) << 4));
-                            *v = make_uint4(v->x ^ 0x80008000u, v->y ^ 0x80008000u, v->z ^ 0x80008000u,
-                                            v->w ^ 0x80008000u);
-                        }
+                        for (int c = 0; c < REP; ++c) copy16(smem_addr(at(y, c)), q_piece(wk, y));
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    if (flip)
+                        for (int y = thread / kCh; y < rows; y += kStep)
+#pragma unroll
+                            for (int c = 0; c < REP; ++c) {
+                                uint4 *v = reinterpret_cast<uint4 *>(at(y, c));
+                                *v = make_uint4(v->x ^ flip, v->y ^ flip, v->z ^ flip, v->w ^ flip);
+                            }
+                }
                 lkd::fence_proxy_async_smem();
                 mbar_arrive(smem_addr(&hd.q_ready));
             }
+            if (kEarly) {
+                ahead.next(p);
+                if (ahead.valid()) load_q(ahead);
+            }
             // positions this row sees: [see0, see1)
             const int64_t pos = int64_t(q.kv) + i;
-            const int64_t see1 = min(pos + 1, q.end);
+            const int64_t see1 = min(pos + 1, int64_t(q.end));
             const int64_t see0 = p.window > 0 ? max(pos - p.window + 1, int64_t(0)) : 0;
             float m = -INFINITY, sum = 0.0f;             // m: the raw product the sums are relative to
             const bool warp_live = (warp % kQuads) * 32 < rows;
@@ -706,10 +755,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     // read twice, for the maximum and for the weights
                     constexpr int kStep = kCols < 32 ? kCols : 32, kSteps = kCols / kStep;
                     constexpr bool kTwice = kCols > 64;
+                    constexpr int kUnroll = kTwice ? 1 : kSteps;
                     const uint32_t at = tmem + lanes + buf * kTile + col0;
                     uint32_t r[kTwice ? 1 : kSteps][kStep];
                     // tiles that some row of the request sees less than all of
-                    const bool masked = x0 + kTile > min(int64_t(q.kv) + 1, q.end) ||
+                    const bool masked = x0 + kTile > min(int64_t(q.kv) + 1, int64_t(q.end)) ||
                                         (p.window > 0 && x0 < int64_t(q.kv) + q.n - p.window);
                     const int c0 = int(min(max(see0 - x0, int64_t(0)), int64_t(kTile))) - col0;
                     const int c1 = int(min(max(see1 - x0, int64_t(0)), int64_t(kTile))) - col0;
@@ -730,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                             mbar_arrive(smem_addr(&hd.s_free));
                         }
                     }
-#pragma unroll
+#pragma unroll kUnroll
                     for (int h = 0; h < kSteps; ++h) {
                         uint32_t (&x)[kStep] = r[kTwice ? 0 : h];
                         if (kTwice) {
@@ -758,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         const float f = !lift ? 1.0f : (m == -INFINITY ? 0.0f : exp2_approx((m - mx) * p.c));
                         if (lift) m = mx;
                         sum *= f;
-#pragma unroll
+#pragma unroll 1
                         for (int j = 0; j < D; j += 32) {
                             uint32_t o[32];
                             tc_ld(tmem + lanes + S::kO + j, o);
@@ -773,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     float part_sum[4] = {};
                     const uint32_t to = tmem + lanes + S::kP + buf * S::kPStep + copy * (kCols / 2);
                     uint32_t w[kTwice ? kStep / 2 : kCols / 2];
-#pragma unroll
+#pragma unroll kUnroll
                     for (int h = 0; h < kSteps; ++h) {
                         uint32_t (&x)[kStep] = r[kTwice ? 0 : h];
                         if (kTwice) {
@@ -817,23 +867,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                 s_at.step(1);
             }
             if (!ok) break;
-            if (!warp_wait(smem_addr(&hd.pv_done[before.at]), before.phase, failed, p.limit)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
             // the item's end: its rows, or this CTA's part of them.  Each thread has a row; 128
-            // bytes of every row of the warp at a time go through shared memory (16-byte
-            // pieces swizzled by the row), so that whole lines are written.
+            // bytes of every row of the warp at a time go through shared memory, in Q's place
+            // (the last S is there, so Q has been read; 16-byte pieces swizzled by the row), so
+            // that whole lines are written.
             const bool whole = wk.a == 0 && wk.b == q.nt;
             const int my_row = lane >> 3, my_piece = lane & 7;       // of four rows at a time
-            // slot 2c + 1: the item began here; 2c: it began in an earlier range
-            const int slot = 2 * cta + (wk.a == 0 ? 1 : 0);
-            float *ws = p.parts + int64_t(slot * REP + copy) * (D + 2) * p.part_rows;
+            float f = 0.0f, all = 0.0f, big = -INFINITY;
             if (REP > 1 && whole) {
-                // the copies' sums added: each at the largest of their m, every copy a part of the
-                // rows (an item that is cut leaves the copies to the join, as parts of their own)
-                float f = 0.0f, all = 0.0f, big = -INFINITY;
+                // the copies' sums are added, each at the largest of their m (an item that is cut
+                // leaves the copies to the join, as parts of their own): their factors, while the
+                // last product runs
                 float *own = reinterpret_cast<float *>(stage);
                 own[lane] = m;
                 own[32 + lane] = sum;
@@ -851,46 +895,66 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                 }
                 if (!(ok = soft_sync())) break;
                 f = all == 0.0f ? 0.0f : f / all;
-#pragma unroll
-                for (int j = 0; j < D; j += 32) {
+            }
+            if (!warp_wait(smem_addr(&hd.pv_done[before.at]), before.phase, failed, p.limit)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // slot 2c + 1: the item began here; 2c: it began in an earlier range
+            const int slot = 2 * cta + (wk.a == 0 ? 1 : 0);
+            float *ws = p.parts + int64_t(slot * REP + copy) * (D + 2) * p.part_rows;
+            if (REP > 1 && whole) {
+                // every copy adds a part of the rows; Q's place holds half of the columns
+                constexpr int kStrips = D / 64;          // of 32 columns, 16 KB each
+#pragma unroll 1
+                for (int j0 = 0; j0 < D; j0 += 32 * kStrips) {
+                    if (j0 > 0 && !(ok = soft_sync())) break;
                     if (warp_live) {
-                        uint32_t o[32];
-                        tc_ld(tmem + lanes + S::kO + j, o);
-                        tc_wait_ld(o);
+#pragma unroll 1
+                        for (int y = 0; y < kStrips; ++y) {
+                            uint32_t o[32];
+                            tc_ld(tmem + lanes + S::kO + j0 + 32 * y, o);
+                            tc_wait_ld(o);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            uint32_t v[4];
+                            for (int k = 0; k < 8; ++k) {
+                                uint32_t v[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v[e] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[4 * k + e]) * f);
-                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                                make_uint4(v[0], v[1], v[2], v[3]);
+                                for (int e = 0; e < 4; ++e)
+                                    v[e] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[4 * k + e]) * f);
+                                *reinterpret_cast<uint4 *>(stage + y * (kRows * 128) + lane * 128 +
+                                                           ((k ^ (lane & 7)) << 4)) =
+                                    make_uint4(v[0], v[1], v[2], v[3]);
+                            }
                         }
                     }
                     if (!(ok = soft_sync())) break;
-#pragma unroll
+#pragma unroll 1
                     for (int t = 0; t < 32 / REP; t += 4) {
                         const int y = copy * (32 / REP) + t + my_row, full_y = (warp % kQuads) * 32 + y;
                         if (full_y < rows) {
-                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                            for (int k = 0; k < REP; ++k) {
-                                const float4 u = *reinterpret_cast<const float4 *>(
-                                    smem + kBarBytes + (warp % kQuads + k * kQuads) * 4096 + y * 128 +
-                                    ((my_piece ^ (y & 7)) << 4));
-                                v.x += u.x;
-                                v.y += u.y;
-                                v.z += u.z;
-                                v.w += u.w;
-                            }
                             const uint32_t ry = wk.mt * kRows + full_y, iy = ry / uint32_t(p.G);
                             const int64_t o_row =
                                 (int64_t(wk.r) * p.N + iy) * p.Hq + wk.h * p.G + (ry - iy * uint32_t(p.G));
-                            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + o_row * D + j + my_piece * 4) =
-                                make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
+#pragma unroll 1
+                            for (int strip = 0; strip < kStrips; ++strip) {
+                                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                                for (int k = 0; k < REP; ++k) {
+                                    const float4 u = *reinterpret_cast<const float4 *>(
+                                        smem + kBarBytes + strip * (kRows * 128) + (warp % kQuads + k * kQuads) * 4096 +
+                                        y * 128 + ((my_piece ^ (y & 7)) << 4));
+                                    v.x += u.x;
+                                    v.y += u.y;
+                                    v.z += u.z;
+                                    v.w += u.w;
+                                }
+                                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + o_row * D + j0 + 32 * strip +
+                                                           my_piece * 4) =
+                                    make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
+                            }
                         }
                     }
-                    if (!(ok = soft_sync())) break;
                 }
                 if (!ok) break;
                 if (live && copy == 0 && p.lse)
@@ -899,9 +963,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             } else if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 if (warp_live) {
-#pragma unroll
+#pragma unroll 1
                     for (int j = 0; j < D; j += 64) {
-#pragma unroll
+#pragma unroll 1
                         for (int half = 0; half < 2; ++half) {
                             uint32_t o[32];
                             tc_ld(tmem + lanes + S::kO + j + 32 * half, o);
@@ -938,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                 }
             } else {
                 if (warp_live) {
-#pragma unroll
+#pragma unroll 1
                     for (int j = 0; j < D; j += 32) {
                         uint32_t o[32];
                         tc_ld(tmem + lanes + S::kO + j, o);
