@@ -80,12 +80,13 @@ struct Shape {
     // Positions of a tile.  The thread that issues the products takes 0.8 us a tile (four
     // waits, a dozen instructions of 40 ns); at D = 64 a tile of 64 positions has 16 KB,
     // for which that is too long (16 requests of 512 to 262144 positions, blocks of 8, 14
-    // heads on 2: 98 us, and 87 in tiles of 128).  At D = 128 and 256 64 positions have 32
+    // heads on 2: 98 us where tiles of 128 took 87).  At D = 128 and 256 64 positions have 32
     // and 64 KB, and 128 would leave less than two tiles of K and V in a CTA's memory.
     static constexpr int kTile = D == 64 ? 128 : 64;
-    // What an item's begin and end cost, in tiles (counted as one tile: the same requests
-    // 101 us for 87, 2048 items of 1 to 2048 positions at D = 128 164 us for 139).
-    static constexpr int kItemUnits = D == 64 ? 8 : D == 128 ? 4 : 6;
+    // What an item's begin and end cost, in tiles.  2048 items of 1 to 2048 positions and 16
+    // rows at D = 128 take 118, 104, 94, 93 us where it is counted as 1, 2, 3, 4 tiles; as
+    // many of 56 rows at D = 64 106, 94, 99, 103 us as 1, 4, 6, 8.
+    static constexpr int kItemUnits = 4;
     // D = 64: K and V share a slot (a wait and a commit less), and one S tile is enough,
     // since P has tensor memory of its own: the next S comes as soon as this one is read.
     // Otherwise two S tiles, P over S, and slots for K and V apart, which fill earlier.
