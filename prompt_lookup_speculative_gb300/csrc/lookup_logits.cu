@@ -1,7 +1,15 @@
 // lookup_logits.cu -- verification of proposal blocks against the target's logits.
 //
-// The contract is in include/lookup_target.h (lookup_verify_logits).  What bounds it:
-// the logits' bytes, each row of 0.3 to 0.6 MB read once.  Two kernels:
+// The contract is in include/lookup_target.h (lookup_verify_logits).
+//
+// The mathematics: p(t) = exp((x_t - m) / T) / s with m the row's maximum and s the sum
+// of the weights, in one pass with a running m: parts (m, s) of a row join as M = max m,
+// sum s exp((m - M) / T).  A proposal d is accepted when u q(d) < p(d).  The token at the
+// first rejection is drawn from the residual max(p - q, 0), the bonus token from p, by a
+// race: the largest of (p - q)(t) / e_t over exponential noise e is at t with that
+// probability, and needs no normalisation and no prefix sums over the vocabulary.
+//
+// What bounds it: the logits' bytes, each row of 0.3 to 0.6 MB read once.  Two kernels:
 // stats_kernel streams every row that a proposal is tested in, cut into segments so
 // that a few rows fill the device, and leaves per segment the running maximum m,
 // s = sum exp((x - m) / T) and (greedy requests) the lowest index of m.
@@ -11,6 +19,12 @@
 // before its first comparison; a second look at one row of P + 1 is cheaper than
 // carrying every row's race through the first pass, where it would read the noise
 // P + 1 times and double the instructions per logit.
+//
+// 64 blocks of 16 over 151936 bf16 logits: 56 us for 272 MB (4.9 TB/s, 72% of a copy's
+// rate), 43 of them the streaming and 13 the draws, which wait for the first kernel's
+// last row and then for a row and its noise.  64 blocks of 8 with a draft distribution
+// over float32 logits 58 us (5.3 TB/s), 8 blocks of 16 over 32000 logits 11.4 us, one
+// greedy block 5.6 us: there both kernels are latency.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
@@ -43,7 +57,7 @@ constexpr int kMaxCtas = 160;            // CTAs of stats_kernel at most, one pe
 constexpr int kPickThreads = 512;
 constexpr int kKept = 32;                // positions whose statistics a CTA of pick_kernel keeps
 constexpr int kMaxCluster = 8;           // CTAs per request in pick_kernel at most
-constexpr int kRace = 16;                // logits in flight per thread there
+constexpr int kRace = 16;                // logits in flight per thread there (8: the draws take longer)
 constexpr int kMaxV = 1 << 30;
 
 struct Params {
@@ -584,7 +598,8 @@ int64_t segments(int32_t B, int32_t P, int32_t V, int size) {
 }
 
 // CTAs of a request's cluster: a power of two, one per 4096 logits of its race as
-// long as all clusters run at once (two CTAs per SM).
+// long as all clusters run at once (two CTAs per SM; with more they run in turns and
+// 64 requests take longer, with one each eight requests' rows would be 8 CTAs' work).
 int cluster_for(int32_t B, int32_t V) {
     int c = 1;
     while (c < kMaxCluster && int64_t(c) * 4096 < V && int64_t(2) * c * B <= 304) c *= 2;
