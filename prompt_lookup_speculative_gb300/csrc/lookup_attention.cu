@@ -23,7 +23,7 @@
 // two (four) times, and each copy's threads take a half (a quarter) of the columns:
 // every quarter of the SM works, and a tile's softmax takes a half (a quarter) of the
 // time.  The product of 16 positions goes into their copy's lanes only, and the
-// copies' sums are added at the end.
+// copies' sums are added at the item's end.
 //
 // Split: the work of all requests, heads and row tiles is laid end to end in units
 // of a tile and cut into equal contiguous ranges, one per CTA (two CTAs per
@@ -106,7 +106,7 @@ struct Shape {
 
 struct Meta {                            // one per CTA: the item it began and did not end
     int32_t r, h, mt, last;              // r = -1: none; last = the CTA that ended it
-    int32_t rows, failed, copies, pad;
+    int32_t rows, failed, pad[2];
 };
 
 struct Params {
@@ -120,7 +120,7 @@ struct Params {
     void *out;
     float *lse;
     Meta *meta;                          // [ctas]
-    float *parts;                        // [2 * ctas][copies]: O [part_rows][D], m [part_rows], sum [part_rows]
+    float *parts;                        // [2 * ctas]: O [part_rows][D], m [part_rows], sum [part_rows]
     uint64_t limit;                      // clocks that a wait may take
 };
 
@@ -642,11 +642,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             return warp_wait(smem_addr(&hd.sync), syncs++ & 1, failed, p.limit);
         };
         unsigned char *stage = smem + kBarBytes + warp * 4096;       // 32 rows of 128 bytes, in Q's place
-        Meta meta{-1, 0, 0, 0, 0, 0, 0, 0};
+        Meta meta{-1, 0, 0, 0, 0, 0, {0, 0}};
         bool ok = true;
         // Q: a thread's pieces of 16 bytes.  Where they are few, the next item's are on their
         // way during this one; otherwise, and where registers are short (two copies at D = 64:
-        // 80 us without, 83 with), they go from global to shared memory by themselves.
+        // 95 us without, 99 with), they go from global to shared memory by themselves.
         constexpr int kCh = D / 8, kStep = kRows / kCh;  // pieces of a row, rows of a pass
         constexpr int kLoads = kRows / REP / kStep;
         constexpr bool kEarly = kLoads <= 4 && !(D == 64 && REP == 2);
@@ -875,10 +875,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             const bool whole = wk.a == 0 && wk.b == q.nt;
             const int my_row = lane >> 3, my_piece = lane & 7;       // of four rows at a time
             float f = 0.0f, all = 0.0f, big = -INFINITY;
-            if (REP > 1 && whole) {
-                // the copies' sums are added, each at the largest of their m (an item that is cut
-                // leaves the copies to the join, as parts of their own): their factors, while the
-                // last product runs
+            if (REP > 1) {
+                // the copies' sums are added, each at the largest of their m: their factors, while
+                // the last product runs
                 float *own = reinterpret_cast<float *>(stage);
                 own[lane] = m;
                 own[32 + lane] = sum;
@@ -895,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     if (k == copy) f = w;
                 }
                 if (!(ok = soft_sync())) break;
-                f = all == 0.0f ? 0.0f : f / all;
+                if (whole) f = all == 0.0f ? 0.0f : f / all;
             }
             if (!warp_wait(smem_addr(&hd.pv_done[before.at]), before.phase, failed, p.limit)) {
                 ok = false;
@@ -904,8 +903,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
             tc_fence_after();
             // slot 2c + 1: the item began here; 2c: it began in an earlier range
             const int slot = 2 * cta + (wk.a == 0 ? 1 : 0);
-            float *ws = p.parts + int64_t(slot * REP + copy) * (D + 2) * p.part_rows;
-            if (REP > 1 && whole) {
+            float *ws = p.parts + int64_t(slot) * (D + 2) * p.part_rows;
+            if (REP > 1) {
                 // every copy adds a part of the rows; Q's place holds half of the columns
                 constexpr int kStrips = D / 64;          // of 32 columns, 16 KB each
 #pragma unroll 1
@@ -950,17 +949,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                                     v.z += u.z;
                                     v.w += u.w;
                                 }
-                                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + o_row * D + j0 + 32 * strip +
-                                                           my_piece * 4) =
-                                    make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
+                                const int at = j0 + 32 * strip + my_piece * 4;
+                                if (whole)
+                                    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + o_row * D + at) =
+                                        make_uint2(pack2(v.x, v.y, T()), pack2(v.z, v.w, T()));
+                                else
+                                    *reinterpret_cast<float4 *>(ws + full_y * D + at) = v;
                             }
                         }
                     }
                 }
                 if (!ok) break;
-                if (live && copy == 0 && p.lse)
-                    p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
-                        all == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(all));
+                if (live && copy == 0) {
+                    if (!whole) {
+                        ws[D * p.part_rows + row] = big;
+                        ws[(D + 1) * p.part_rows + row] = all;
+                    } else if (p.lse) {
+                        p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
+                            all == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(all));
+                    }
+                }
             } else if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 if (warp_live) {
@@ -1036,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     int64_t last = (end - 1) * ctas / total;
                     while (last + 1 < ctas && total * (last + 1) / ctas <= end - 1) ++last;
                     while (total * last / ctas > end - 1) --last;
-                    meta = Meta{wk.r, wk.h, wk.mt, int32_t(last), rows, 0, REP, 0};
+                    meta = Meta{wk.r, wk.h, wk.mt, int32_t(last), rows, 0, {0, 0}};
                 }
             }
             tc_fence_before();                           // O is read before the next item's products (p_ready)
@@ -1057,8 +1065,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
 
 template <int D, int ROWS>
 struct JoinSmem {
-    static constexpr int kMost = kMaxSms * Shape<D>::kCtas;          // ranges at most, of up to 4 copies
-    float weights[ROWS][4 * kMost], big[ROWS], sum[ROWS];
+    static constexpr int kMost = kMaxSms * Shape<D>::kCtas;          // ranges at most
+    float weights[ROWS][kMost], big[ROWS], sum[ROWS];
     float sums[kJoinWarps][ROWS][D];
     Meta metas[kMost];
 };
@@ -1075,13 +1083,8 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D, 
     constexpr int kFirst = 512 / D / ROWS > 0 ? 512 / D / ROWS * (D == 256 ? 1 : 2) : 1;     // parts of a warp in flight
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t size = int64_t(D + 2) * p.part_rows;   // of a part
-    // the slot 2c + 1, then every second one after 2c + 2, each with its copies
-    const int copies = meta.copies, shift = copies == 4 ? 2 : copies == 2 ? 1 : 0;
-    const int count = (meta.last - c + 1) * copies;
-    auto part = [&](int k) {
-        const int range = k >> shift, slot = range ? 2 * (c + range) : 2 * c + 1;
-        return p.parts + int64_t((slot << shift) + (k & (copies - 1))) * size;
-    };
+    const int count = meta.last - c + 1;                 // the slot 2c + 1, then every second one after 2c + 2
+    auto part = [&](int k) { return p.parts + int64_t(k ? 2 * (c + k) : 2 * c + 1) * size; };
     auto place = [&](int row) {                          // the row's place in out / D and in lse
         const int rr = meta.mt * kRows + row, i = rr / p.G;
         return (int64_t(meta.r) * p.N + i) * p.Hq + meta.h * p.G + (rr - i * p.G);
@@ -1254,7 +1257,7 @@ int copies_for(int64_t N, int64_t G) { return N * G <= 32 ? 4 : N * G <= 64 ? 2 
 size_t workspace_for(int32_t N, int32_t G, int32_t D) {
     const size_t ctas = size_t(ctas_for(D, kMaxSms));
     return ctas * sizeof(Meta) +
-           ctas * 2 * size_t(copies_for(N, G)) * size_t(D + 2) * size_t(part_rows_for(N, G)) * sizeof(float);
+           ctas * 2 * size_t(D + 2) * size_t(part_rows_for(N, G)) * sizeof(float);
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1292,13 +1295,8 @@ int cache_map(EncodeTiled fn, CUtensorMap *map, const void *base, int32_t type, 
 template <typename T, int D>
 int launch(Params &p, cudaStream_t stream) {
     using S = Shape<D>;
-    // Every copy of an item that is cut is a part of its own.  A few long items are cut into
-    // tens of parts, and half as many are faster than a softmax over a quarter of the
-    // columns: 8 items of 4096 positions at D = 128 take 16.0 us with two copies and 17.9
-    // with four, 2 of 30000 at D = 64 28 and 35.  With more items four are: 16 of 3000
-    // positions 15.4 and 15.9 us, 2048 of 1 to 2048 138 us and 156 (and 175 with one copy).
     const int64_t items = int64_t(p.B) * p.Hkv * ((int64_t(p.N) * p.G + kRows - 1) / kRows);
-    const int copies = std::min(copies_for(p.N, p.G), items < 16 ? 2 : 4);
+    const int copies = copies_for(p.N, p.G);
     auto kernel = copies == 4 ? attention_kernel<T, D, 4> : copies == 2 ? attention_kernel<T, D, 2> : attention_kernel<T, D, 1>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "shared-memory opt-in");
