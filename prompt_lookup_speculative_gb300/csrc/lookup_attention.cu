@@ -36,7 +36,14 @@
 // Short items: what runs once per item, at its begin and end, waits for its instructions
 // more than for anything else, so that code is kept small: loops there are rolled, one
 // copy of each step.  The next item's Q and first page ids are loaded during an item.
-// 2048 items of 1 to 2048 positions, 4 heads each at D = 128: 138 us before, 87 after.
+// 2048 items of 1 to 2048 positions, 4 heads each at D = 128: 138 us before, 83 with that
+// (3.9 TB/s, 57% of a copy's rate).
+//
+// Long ones: 64 blocks of 16 tokens over 25000 positions, 32 heads on 4 at D = 128, 505 us
+// (6.5 TB/s, 96% of a copy's rate), one token each over 12000 to 25000 667 us (7.0 TB/s).
+// 16 blocks of 8 over 512 to 262144, 14 heads on 2 at D = 64, 79 us (5.0 TB/s): the
+// instructions that issue a tile's products take as long as its 32 KB.  One token over 4096
+// positions 15.3 us: the way through both kernels, once.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
@@ -68,7 +75,7 @@ constexpr int kSoftWarps = 4;            // one thread per row
 constexpr int kLoadWarp = 4, kMmaWarp = 5;
 constexpr int kThreads = 192;
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;       // of a CTA of join_kernel
-constexpr int kFewParts = 4;             // parts that a warp joins by itself (1: 512 items of 48 rows 270 us, not 260)
+constexpr int kFewParts = 4;             // parts that a warp joins by itself (1: 512 items of 48 rows 265 us, not 255)
 constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
 constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
 constexpr int kBarBytes = 1024;          // barriers and small state ahead of the tiles
@@ -80,12 +87,12 @@ struct Shape {
     // Positions of a tile.  The thread that issues the products takes 0.8 us a tile (four
     // waits, a dozen instructions of 40 ns); at D = 64 a tile of 64 positions has 16 KB,
     // for which that is too long (16 requests of 512 to 262144 positions, blocks of 8, 14
-    // heads on 2: 98 us where tiles of 128 took 87).  At D = 128 and 256 64 positions have 32
+    // heads on 2: 97 us, and 79 in tiles of 128).  At D = 128 and 256 64 positions have 32
     // and 64 KB, and 128 would leave less than two tiles of K and V in a CTA's memory.
     static constexpr int kTile = D == 64 ? 128 : 64;
-    // What an item's begin and end cost, in tiles.  2048 items of 1 to 2048 positions and 16
-    // rows at D = 128 take 118, 104, 94, 93 us where it is counted as 1, 2, 3, 4 tiles; as
-    // many of 56 rows at D = 64 106, 94, 99, 103 us as 1, 4, 6, 8.
+    // What an item's begin and end cost, in tiles.  2048 items of 1 to 2048 positions and 32
+    // rows at D = 128 take 100, 90, 87, 94 us where it is counted as 2, 3, 4, 6 tiles; as many
+    // of 56 rows at D = 64 99, 96, 95, 99 us, 512 of 32 rows at D = 256 69, 64, 61, 65.
     static constexpr int kItemUnits = 4;
     // D = 64: K and V share a slot (a wait and a commit less), and one S tile is enough,
     // since P has tensor memory of its own: the next S comes as soon as this one is read.
@@ -1250,8 +1257,10 @@ int ctas_for(int D, int sms) { return sms * (D == 256 ? 1 : 2); }
 // Rows of a part: even, so that every part's rows are 16-byte aligned.
 int part_rows_for(int64_t N, int64_t G) { return int(N * G < kRows ? (N * G + 1) / 2 * 2 : kRows); }
 
-// Copies of the block's rows in a tile at most: those that fit a half or a quarter of it
-// are there twice or four times.
+// Copies of the block's rows in a tile: those that fit a half or a quarter of it are there
+// twice or four times.  2048 items of 1 to 2048 positions at D = 128, 16 rows: 126, 98, 86 us
+// with one, two, four; 32 items of 48000 at D = 64, 56 rows: 85 us with one, 77 with two.
+// (One token over 4096 positions, 2 tiles a CTA, would gain by one copy: 14.5 us for 15.3.)
 int copies_for(int64_t N, int64_t G) { return N * G <= 32 ? 4 : N * G <= 64 ? 2 : 1; }
 
 size_t workspace_for(int32_t N, int32_t G, int32_t D) {
@@ -1314,12 +1323,13 @@ int launch(Params &p, cudaStream_t stream) {
     if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
     lookup_note_launch();
     // The join.  With about as many items as ranges each is cut once or twice, and a few
-    // CTAs an item do; a few long items have tens of parts and take 16 (32 items of 56 rows
-    // at D = 64: the whole call 87 us, and 108 with 4).  A CTA takes four rows at a time; one
-    // where all items together have few rows (8 items of 4: 17.9 us, and 19.4 by fours; 4 of
-    // 128: 45 us by fours, and 67).  Where those CTAs times the ranges would be several waves
-    // of mostly idle ones, fewer CTAs share the ranges (those 32 items: 87 us, and 91 with a
-    // CTA for each range; an odd number: evenly cut items begin at even distances).
+    // CTAs an item do (256 items of 128 rows: the whole call 506 us, and 514 with 16); a few
+    // long items have tens of parts and take 16 (32 items of 56 rows at D = 64: 79 us, and 90
+    // with 4).  A CTA takes four rows at a time; one where all items together have few rows
+    // (8 items of 16 rows at D = 256: 19.1 us, and 20.4 by fours; 4 of 128 rows: 41 us by fours,
+    // and 62).  Where those CTAs times the ranges would be several waves of mostly idle ones,
+    // fewer CTAs share the ranges (those 32 items: 79 us, and 83 with CTAs for each range; an
+    // odd number: evenly cut items begin at even distances).
     const bool single = items * p.part_rows < 512;
     const int per = std::min(single ? p.part_rows : (p.part_rows + 3) / 4, 3 * items >= p.ctas ? 4 : 16);
     const int64_t over = int64_t(per) * p.ctas <= 1216 ? p.ctas : std::min<int64_t>(p.ctas, 2 * items + 1);
