@@ -230,6 +230,18 @@ def test_attention_of_many_tiles_per_range(D, N, Hq, Hkv, page, window):
     check_attention(*filled_case(lens, qn, N, Hq, Hkv, D, page, BF16, D + N), window=window)
 
 
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 0.11])
+@pytest.mark.parametrize("D,N,Hq,Hkv,page,window", [
+    (64, 2, 7, 1, 16, 3), (64, 7, 14, 2, 32, 700), (128, 2, 16, 2, 8, 5), (128, 6, 16, 2, 64, 1100), (256, 3, 8, 2, 16, 40),
+    (256, 16, 16, 2, 128, 900)])
+def test_attention_of_cut_items_under_a_window(D, N, Hq, Hkv, page, window, scale):
+    """Items cut between ranges where some of a row's parts hold nothing that it sees,
+    for one, two and four copies of the block's rows, and scales of either sign."""
+    lens = [2900, 2047, 1, 0, 1025, 64, 800, 2500]
+    qn = [N, 1, N, 0, (N + 1) // 2, N, 1, N]
+    check_attention(*filled_case(lens, qn, N, Hq, Hkv, D, page, F16, D + N + window), scale=scale, window=window)
+
+
 def test_attention_many_requests_of_mixed_length():
     g = gen(9)
     lens = torch.randint(0, 90, (700,), generator=g).tolist()
