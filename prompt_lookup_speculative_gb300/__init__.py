@@ -942,7 +942,10 @@ _target_module = None
 def _target():
     """The compiled entry of these calls (csrc/target_binding.cpp): it checks the tensors,
     allocates what is not given and enters the library, in a fraction of the time that
-    takes from Python, which for these kernels would be longer than they run."""
+    takes from Python, which for these kernels would be longer than they run.
+
+    With ``stream=`` the call runs on that stream, and so do the outputs and workspace that
+    it allocates; order that stream after what made the inputs, and yours after it."""
     global _target_module
     if _target_module is None:
         import importlib.util

@@ -82,13 +82,6 @@ const void *strided(const at::Tensor &t, const char *name, at::ScalarType type, 
     return t.data_ptr();
 }
 
-// The caller's output, checked, or a new one.
-at::Tensor output(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef shape, const c10::Device &dev) {
-    if (o == Py_None) return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
-    dense(o, name, type, shape, dev);
-    return THPVariable_Unpack(o);
-}
-
 int32_t size32(int64_t x, const char *name) {
     if (x > INT32_MAX) refuse(std::string(name) + " has 2^31 elements or more along an axis");
     return int32_t(x);
@@ -113,36 +106,65 @@ long whole(PyObject *o, const char *name) {
     return x;
 }
 
-// The given torch.cuda.Stream, or the device's current one.
-c10::cuda::CUDAStream stream_of(PyObject *o, const c10::Device &dev) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index());
-    int64_t v[3];
-    const char *names[3] = {"stream_id", "device_index", "device_type"};
-    for (int k = 0; k < 3; ++k) {
-        PyObject *a = PyObject_GetAttrString(o, names[k]);
-        if (!a) throw python_error();
-        v[k] = PyLong_AsLongLong(a);
-        Py_DECREF(a);
-        if (v[k] == -1 && PyErr_Occurred()) throw python_error();
+// The stream of a call: the given torch.cuda.Stream, made current, or the device's current
+// one.  PyTorch's allocator keeps memory per stream, so what a call allocates comes from
+// its own stream's: other streams' may still be in use by work that they have queued.
+class On {
+    c10::cuda::CUDAGuard device_;
+    c10::cuda::OptionalCUDAStreamGuard current_;
+
+public:
+    const c10::Device dev;
+    const c10::cuda::CUDAStream caller;                  // current when the call was made
+    const c10::cuda::CUDAStream stream;
+
+    On(PyObject *o, const c10::Device &d)
+        : device_(d), dev(d), caller(c10::cuda::getCurrentCUDAStream(d.index())), stream(given(o, caller)) {
+        if (stream.device() != dev) refuse("stream must be of the tensors' device, " + dev.str());
+        if (stream != caller) current_.reset_stream(stream);
     }
-    return c10::cuda::CUDAStream::unpack3(v[0], c10::DeviceIndex(v[1]), c10::DeviceType(v[2]));
+
+private:
+    static c10::cuda::CUDAStream given(PyObject *o, const c10::cuda::CUDAStream &caller) {
+        if (o == Py_None) return caller;
+        int64_t v[3];
+        const char *names[3] = {"stream_id", "device_index", "device_type"};
+        for (int k = 0; k < 3; ++k) {
+            PyObject *a = PyObject_GetAttrString(o, names[k]);
+            if (!a) throw python_error();
+            v[k] = PyLong_AsLongLong(a);
+            Py_DECREF(a);
+            if (v[k] == -1 && PyErr_Occurred()) throw python_error();
+        }
+        return c10::cuda::CUDAStream::unpack3(v[0], c10::DeviceIndex(v[1]), c10::DeviceType(v[2]));
+    }
+};
+
+// The caller's output, checked, or a new one: of the call's stream, and not used again
+// before the caller's stream is past what it does with it.
+at::Tensor output(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef shape, const On &on) {
+    if (o != Py_None) {
+        dense(o, name, type, shape, on.dev);
+        return THPVariable_Unpack(o);
+    }
+    at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(on.dev));
+    if (on.stream != on.caller && t.numel()) t.record_stream(on.caller.unwrap());
+    return t;
 }
 
-// The call's workspace: the caller's, or one from PyTorch's allocator that stays
-// reserved until the stream is past the call.
+// The call's workspace: the caller's, or one of the call's stream, where whatever takes its
+// memory next runs after the call.
 struct Workspace {
     at::Tensor t;
     size_t bytes;
 };
-Workspace workspace(PyObject *o, size_t bytes, const c10::Device &dev, const c10::cuda::CUDAStream &stream, bool given) {
+Workspace workspace(PyObject *o, size_t bytes, const On &on) {
     if (o != Py_None) {
         const at::Tensor &t = tensor(o, "workspace");
-        if (t.device() != dev || !t.is_contiguous()) refuse("workspace must be a contiguous tensor on " + dev.str());
+        if (t.device() != on.dev || !t.is_contiguous()) refuse("workspace must be a contiguous tensor on " + on.dev.str());
         return {t, size_t(t.numel()) * t.element_size()};
     }
-    at::Tensor t = at::empty({int64_t(bytes)}, at::TensorOptions().dtype(at::kByte).device(dev));
-    if (given && bytes) t.record_stream(stream.unwrap());
-    return {t, bytes};
+    return {at::empty({int64_t(bytes)}, at::TensorOptions().dtype(at::kByte).device(on.dev)), bytes};
 }
 
 // The interpreter's lock released while the library enqueues.
@@ -219,9 +241,8 @@ PyObject *kv_append(PyObject *const *a, Py_ssize_t n) {
     }
     const int interleaved = PyObject_IsTrue(a[9]);
     if (interleaved < 0) throw python_error();
-    c10::cuda::CUDAGuard guard(dev);
-    const c10::cuda::CUDAStream stream = stream_of(a[12], dev);
-    at::Tensor outs[2] = {output(a[10], "out_q", type, {B, N, hq, D}, dev), output(a[11], "status", at::kInt, {B}, dev)};
+    const On on(a[12], dev);
+    at::Tensor outs[2] = {output(a[10], "out_q", type, {B, N, hq, D}, on), output(a[11], "status", at::kInt, {B}, on)};
     if (N == 0) outs[1].zero_();
     int rc;
     {
@@ -229,7 +250,7 @@ PyObject *kv_append(PyObject *const *a, Py_ssize_t n) {
         rc = g_kv_append(qp, qs, kp, ks, vp, vs, c.kv_len, c.q_len, c.table, size32(B, "q"), size32(N, "q"),
                          size32(hq, "q"), c.hkv, size32(D, "q"), c.max_pages, c.pages, c.page, rotary, rot, max_pos,
                          interleaved, code, c.k, c.v, outs[0].data_ptr(), static_cast<int32_t *>(outs[1].data_ptr()),
-                         stream.stream());
+                         on.stream.stream());
     }
     return result(rc, outs, 2);
 }
@@ -249,16 +270,15 @@ PyObject *attention(PyObject *const *a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw python_error();
     const int32_t window = int32_t(whole(a[7], "window"));
     const int32_t b = size32(B, "q"), t = size32(N, "q"), h = size32(hq, "q"), d = size32(D, "q");
-    c10::cuda::CUDAGuard guard(dev);
-    const c10::cuda::CUDAStream stream = stream_of(a[11], dev);
-    at::Tensor outs[2] = {output(a[8], "out", type, {B, N, hq, D}, dev), output(a[9], "lse", at::kFloat, {B, N, hq}, dev)};
-    const Workspace ws = workspace(a[10], g_attention_bytes(b, t, h, c.hkv, d), dev, stream, a[11] != Py_None);
+    const On on(a[11], dev);
+    at::Tensor outs[2] = {output(a[8], "out", type, {B, N, hq, D}, on), output(a[9], "lse", at::kFloat, {B, N, hq}, on)};
+    const Workspace ws = workspace(a[10], g_attention_bytes(b, t, h, c.hkv, d), on);
     int rc;
     {
         Unlocked unlocked;
         rc = g_attention(qp, qs, c.k, c.v, c.table, c.kv_len, c.q_len, b, t, h, c.hkv, d, c.max_pages, c.pages, c.page,
                          float(scale), window, code, outs[0].data_ptr(), static_cast<float *>(outs[1].data_ptr()),
-                         ws.t.data_ptr(), ws.bytes, stream.stream());
+                         ws.t.data_ptr(), ws.bytes, on.stream.stream());
     }
     return result(rc, outs, 2);
 }
@@ -281,19 +301,18 @@ PyObject *verify(PyObject *const *a, Py_ssize_t n) {
     const int32_t *blk = dense<int32_t>(a[0], "block", at::kInt, {B, P}, dev);
     const int32_t *len = dense<int32_t>(a[1], "len", at::kInt, {B}, dev);
     const int32_t b = size32(B, "block"), p = size32(P, "block"), v = size32(V, "logits");
-    c10::cuda::CUDAGuard guard(dev);
-    const c10::cuda::CUDAStream stream = stream_of(a[13], dev);
-    at::Tensor outs[4] = {output(a[8], "accepted", at::kInt, {B}, dev), output(a[9], "commit", at::kInt, {B, P + 1}, dev),
-                          output(a[10], "ncommit", at::kInt, {B}, dev),
-                          output(a[11], "logprobs", at::kFloat, {B, P + 1}, dev)};
-    const Workspace ws = workspace(a[12], g_verify_bytes(b, p, v), dev, stream, a[13] != Py_None);
+    const On on(a[13], dev);
+    at::Tensor outs[4] = {output(a[8], "accepted", at::kInt, {B}, on), output(a[9], "commit", at::kInt, {B, P + 1}, on),
+                          output(a[10], "ncommit", at::kInt, {B}, on),
+                          output(a[11], "logprobs", at::kFloat, {B, P + 1}, on)};
+    const Workspace ws = workspace(a[12], g_verify_bytes(b, p, v), on);
     int rc;
     {
         Unlocked unlocked;
         rc = g_verify(blk, len, lp, ls, code, v, noise, temperature, u, static_cast<const float *>(qprobs), qs, point, b,
                       p, static_cast<int32_t *>(outs[0].data_ptr()), static_cast<int32_t *>(outs[1].data_ptr()),
                       static_cast<int32_t *>(outs[2].data_ptr()), static_cast<float *>(outs[3].data_ptr()),
-                      ws.t.data_ptr(), ws.bytes, stream.stream());
+                      ws.t.data_ptr(), ws.bytes, on.stream.stream());
     }
     return result(rc, outs, 4);
 }

@@ -1,5 +1,6 @@
 """The target's operators (include/lookup_target.h) where their arithmetic and their
-memory are most easily wrong: temperatures down to float32's smallest, logits of 1e8.
+memory are most easily wrong: temperatures down to float32's smallest, logits of 1e8,
+streams other than the current one.
 
 The definitions and bounds are those of target_reference.py, as in test_gpu_target.py.
 """
@@ -10,7 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pkg = pytest.importorskip("prompt_lookup_speculative_gb300")
 
-from test_gpu_target import BF16, F16, F32, check_verify, gen  # noqa: E402
+from test_gpu_target import BF16, F16, F32, attention_case, check_verify, gen, verify_case  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,74 @@ def test_verify_large_finite_logits(size, T):
         c["noise"] = c["u"] = c["temperature"] = None
     _, _, _, lps = check_verify(c, least=0.6)
     assert bool(lps.isfinite().all())
+
+
+# ----------------------------------------------------------------- streams ----
+def calls_on(stream):
+    """The three calls on `stream` (None: the current one), each as a function of nothing."""
+    q, kc, vc, table, kv, ql = (x.cuda() for x in attention_case([700, 1500], [16, 16], 16, 8, 2, 128, 16, BF16, 3))
+    c = {k: None if v is None else v.cuda() for k, v in verify_case(8, 15, 9001, BF16, "point", 5).items()}
+    k = kc[:2, :, :, :].reshape(2, 16, 2, 128)
+    into = torch.zeros_like(kc), torch.zeros_like(vc)
+    return {
+        "attention": lambda: pkg.lookup_paged_attention(q, kc, vc, table, kv, q_len=ql, stream=stream),
+        "verify": lambda: pkg.lookup_verify_logits(c["block"], c["length"], c["logits"], noise=c["noise"], u=c["u"],
+                                                   temperature=c["temperature"], stream=stream),
+        "append": lambda: pkg.lookup_kv_append(q, k, k, kv, table, *into, stream=stream),
+    }
+
+
+@pytest.mark.parametrize("name", ["attention", "verify", "append"])
+def test_another_streams_call_leaves_released_memory_alone(name):
+    """Tensors of the current stream that were released while work that reads them waits: a
+    call on another stream must not write there, be it outputs or its workspace."""
+    side = torch.cuda.Stream()
+    call, want = calls_on(side)[name], calls_on(None)[name]()
+    torch.cuda.synchronize()
+    sizes = [t.numel() * t.element_size() for t in want] + [
+        pkg.load_library().lookup_paged_attention_workspace_bytes(2, 16, 8, 2, 128),
+        pkg.load_library().lookup_verify_logits_workspace_bytes(8, 15, 9001)]
+    torch.cuda.empty_cache()
+    kept = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(40)]
+    released = [torch.full_like(t, 0x5A) for t in kept]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                     # 0.1 s of the current stream
+    for to, t in zip(kept, released):
+        to.copy_(t)
+    del released, t
+    got = call()
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    torch.cuda.synchronize()
+    assert all(bool((t == 0x5A).all()) for t in kept)
+
+
+def test_an_output_released_early_is_not_used_again():
+    """The output of a call on another stream, read by the current one and released before
+    that has happened: the next calls there must leave it alone."""
+    side = torch.cuda.Stream()
+    call = calls_on(side)["attention"]
+    torch.cuda.synchronize()
+    out, lse = call()
+    torch.cuda.current_stream().wait_stream(side)
+    want = out.clone()
+    torch.cuda.synchronize()
+    kept = torch.zeros_like(out)
+    torch.cuda._sleep(200_000_000)
+    kept.copy_(out)
+    del out, lse
+    with torch.cuda.stream(side):
+        for _ in range(20):                            # whoever takes memory of that stream next
+            torch.full_like(kept, 7.0)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Elsewhere:
+        stream_id, device_index, device_type = 0, 1, 1
+
+    for call in calls_on(Elsewhere()).values():
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert torch.cuda.current_device() == 0
