@@ -96,7 +96,10 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
  *
  * Token i < q_len[r], at position p = kv_len[r] + i, sees positions j <= p (and
  * j > p - window).  With s_j = scale * q.k_j in float32: lse = log(sum_j
- * exp(s_j)), out = sum_j exp(s_j - lse) v_j.  Rows past q_len[r] have out = 0 and
+ * exp(s_j)), out = sum_j exp(s_j - lse) v_j.  The weights are rounded to `type` for
+ * their product with v (relative 2^-8 for bfloat16; 2^-11 for float16, where those
+ * below 2^-21 of the largest are off by up to 2^-32 of it), and lse takes them before
+ * that; everything else is float32.  Rows past q_len[r] have out = 0 and
  * lse = -infinity.  A request's tokens past the block table's end are taken as
  * absent, and a table entry outside [0, pages) as a page of zeros; slots that no
  * token of the request sees are never used, whatever they hold.  A value in v_cache

@@ -15,8 +15,11 @@
 // them exactly; fewer rows leave lanes idle, which costs no bytes): S = Q K^T of 128
 // rows by a tile of 64 or 128 positions into tensor memory, softmax by one thread per
 // row, P back into tensor memory, O += P V from there.  P is rounded to the cache's type,
-// as the product's operand has to be (relative 2^-9 or 2^-12, the rounding of an output);
-// the sum takes the weights before that, and S, O, m and the sum are float32.
+// as the product's operand has to be (relative 2^-8 in bfloat16, 2^-11 in float16, as an
+// output is); the sum takes the weights before that, and S, O, m and the sum are float32.
+// float16's weights are taken 2^7 higher, for which there is room above 2^8: those down to
+// 2^-21 of m's keep that rounding, and only below 2^-32 do they leave the product (2^-14
+// and 2^-25 without: behind one score 17 above it, a long even tail counted 1.4 times).
 //
 // Few rows: the tile has idle rows, and only the warps of the live ones have a softmax
 // to do, one SM quarter per 32 rows.  So a block of at most 64 (32) rows is in the tile
@@ -58,6 +61,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 namespace {
 
@@ -78,6 +82,10 @@ constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;       // of a CTA 
 constexpr int kFewParts = 4;             // parts that a warp joins by itself (1: 512 items of 48 rows 265 us, not 255)
 constexpr int kMaxSms = 160;             // the workspace is sized for this many (a GB300 has 152)
 constexpr float kLazy = 8.0f;            // log2 of how far m may lag behind a row's maximum
+// log2 of the factor that all weights (and so their sum) carry: float16's 2^-24 steps end
+// that much further down, and 2^(kLazy + 7) is still in its range
+template <typename T>
+constexpr float kRaise = std::is_same<T, __half>::value ? 7.0f : 0.0f;
 constexpr int kBarBytes = 1024;          // barriers and small state ahead of the tiles
 
 // Shared memory and tensor memory of head size D.  A slot holds one tile of K, of V or of both.
@@ -827,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                             tc_st(tmem + lanes + S::kO + j, o);
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * p.c;
+                    const float base = kRaise<T> - (m == -INFINITY ? 0.0f : m * p.c);
                     float part_sum[4] = {};
                     const uint32_t to = tmem + lanes + S::kP + buf * S::kPStep + copy * (kCols / 2);
                     uint32_t w[kTwice ? kStep / 2 : kCols / 2];
@@ -845,8 +853,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         }
 #pragma unroll
                         for (int j = 0; j < kStep; j += 2) {
-                            float a0 = exp2_approx(fmaf(__uint_as_float(x[j]), p.c, -mc));
-                            float a1 = exp2_approx(fmaf(__uint_as_float(x[j + 1]), p.c, -mc));
+                            float a0 = exp2_approx(fmaf(__uint_as_float(x[j]), p.c, base));
+                            float a1 = exp2_approx(fmaf(__uint_as_float(x[j + 1]), p.c, base));
                             if (masked) {                // also where c is 0
                                 a0 = x[j] == 0xff800000u ? 0.0f : a0;
                                 a1 = x[j + 1] == 0xff800000u ? 0.0f : a1;
@@ -973,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                         ws[(D + 1) * p.part_rows + row] = all;
                     } else if (p.lse) {
                         p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
-                            all == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(all));
+                            all == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + (log2f(all) - kRaise<T>));
                     }
                 }
             } else if (whole) {
@@ -1014,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) attention_kernel(co
                     }
                     if (live && p.lse)
                         p.lse[(int64_t(wk.r) * p.N + i) * p.Hq + head] =
-                            sum == 0.0f ? -INFINITY : 0.6931471805599453f * (m * p.c + log2f(sum));
+                            sum == 0.0f ? -INFINITY : 0.6931471805599453f * (m * p.c + (log2f(sum) - kRaise<T>));
                 }
             } else {
                 if (warp_live) {
@@ -1102,7 +1110,7 @@ __device__ void join_item(const Params &p, int c, const Meta &meta, JoinSmem<D, 
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) dst[e] = sum == 0.0f ? 0u : pack2(o[2 * e] * inv, o[2 * e + 1] * inv, T());
         if (lane == 0 && p.lse)
-            p.lse[place(row)] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + log2f(sum));
+            p.lse[place(row)] = sum == 0.0f ? -INFINITY : 0.6931471805599453f * (big * p.c + (log2f(sum) - kRaise<T>));
     };
     if (count <= kFewParts) {
         constexpr int kPair = D == 256 ? 1 : 2;          // rows at a time

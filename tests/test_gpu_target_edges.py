@@ -1,6 +1,6 @@
 """The target's operators (include/lookup_target.h) where their arithmetic and their
 memory are most easily wrong: temperatures down to float32's smallest, logits of 1e8,
-streams other than the current one.
+weights far below a row's largest, streams other than the current one.
 
 The definitions and bounds are those of target_reference.py, as in test_gpu_target.py.
 """
@@ -61,6 +61,50 @@ def test_verify_large_finite_logits(size, T):
         c["noise"] = c["u"] = c["temperature"] = None
     _, _, _, lps = check_verify(c, least=0.6)
     assert bool(lps.isfinite().all())
+
+
+# --------------------------------------------------------------- attention ----
+@pytest.mark.parametrize("dt", [F16, BF16])
+@pytest.mark.parametrize("gap", [12.0, 16.0, 17.0, 17.5, 19.0, 21.0])
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,L", [(40, 1, 8, 8, 64, 16384), (1, 1, 1, 1, 128, 40000), (76, 6, 32, 4, 128, 5000),
+                                            (40, 16, 64, 8, 64, 9000), (40, 3, 16, 4, 256, 4001)])
+def test_attention_long_tail_behind_one_large_score(dt, gap, B, N, Hq, Hkv, D, L):
+    """One position `gap` nats above all the others, which hold v = 1 where it holds 0: the
+    output is what the others' small weights come to.  A weight w (the largest is 1) may
+    be off by its rounding to the type, or in float16 by half a step of 2^-24 / 2^7."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(int(gap * 2) + D)
+    page, u = 64, 2.0 ** -11 if dt == F16 else 2.0 ** -8
+    width = -(-(L + N) // page)
+    kc = torch.randn((B * width, Hkv, page, D), device="cuda", generator=g).to(dt)
+    kc[..., 0] = (0.25 * torch.randn(kc.shape[:3], device="cuda", generator=g)).clamp(-1, 1).to(dt)
+    vc = torch.ones_like(kc)
+    vc[..., 1] = torch.rand(kc.shape[:3], device="cuda", generator=g).to(dt)
+    table = torch.randperm(B * width, device="cuda", generator=g).to(torch.int32).view(B, width)
+    at = torch.randint(L, (B,), device="cuda", generator=g)
+    first = table[torch.arange(B, device="cuda"), at // page].long()
+    kc[first, :, at % page, 0] = gap
+    vc[first, :, at % page] = 0.0
+    q = torch.zeros((B, N, Hq, D), device="cuda", dtype=dt)
+    q[..., 0] = D ** 0.5 if D != 128 else 8.0            # the score is a key's first element
+    scale = D ** -0.5 if D != 128 else 0.125
+    out, lse = pkg.lookup_paged_attention(q, kc, vc, table, torch.full((B,), L, dtype=torch.int32, device="cuda"), scale=scale)
+    torch.cuda.synchronize()
+    pos = torch.arange(width * page, device="cuda")
+    see = pos <= L + torch.arange(N, device="cuda")[:, None]
+    tiny = 2.0 ** -32 if dt == F16 else 0.0
+    for b in range(0, B, 7):
+        k0 = kc[table[b].long()][..., 0].transpose(0, 1).reshape(Hkv, 1, -1).double()      # [Hkv, 1, positions]
+        v = vc[table[b].long()].transpose(0, 1).reshape(Hkv, -1, D).double()
+        w = torch.where(see, (k0 - gap).exp(), 0.0)                                        # [Hkv, N, positions]
+        z = w.sum(-1, keepdim=True)
+        o = (w / z) @ v
+        lost = (torch.minimum(w, torch.full_like(w, tiny)) + w * u) / z @ v
+        bound = lost * 1.01 + o * (u + 2.0 ** -18 + (L + 64) * 2.0 ** -24) + 2.0 ** -25
+        o, bound = (x.repeat_interleave(Hq // Hkv, 0).transpose(0, 1) for x in (o, bound))
+        assert bool(((out[b].double() - o).abs() <= bound).all()), float(((out[b].double() - o).abs() / bound).max())
+        one = (gap + z[..., 0].log()).repeat_interleave(Hq // Hkv, 0).T
+        assert bool(((lse[b].double() - one).abs() <= one.abs() * 2.0 ** -22 + (L + 64) * 2.0 ** -24).all())
 
 
 # ----------------------------------------------------------------- streams ----
