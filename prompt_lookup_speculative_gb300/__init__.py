@@ -954,6 +954,8 @@ def _target():
         lib = load_library()
         with _lib_lock:
             path = _build.binding_path()
+            if path is None:
+                raise RuntimeError("the target's operators need a PyTorch built with CUDA")
             if not os.path.exists(path):
                 raise RuntimeError(f"the compiled binding {path} is missing; run build() first")
             spec = importlib.util.spec_from_file_location("_target", path)

@@ -69,16 +69,23 @@ def compile_command(out: str, extra: list[str] | None = None, checked: bool = Fa
             "-I", INCLUDE_DIR, *defines, "-o", out, *sources, *(extra or [])]
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None else None
+
+
 def binding_path() -> str | None:
-    """Where the target operators' Python entry is built; None without PyTorch."""
-    if importlib.util.find_spec("torch") is None:
+    """Where the target operators' Python entry is built; None without PyTorch, or with one
+    that was built without CUDA."""
+    torch_dir = _torch_dir()
+    if torch_dir is None or not os.path.exists(os.path.join(torch_dir, "lib", "libc10_cuda.so")):
         return None
     return os.path.join(BUILD_DIR, f"_target-{importlib.metadata.version('torch')}.so")
 
 
 def binding_command(out: str) -> list[str]:
     """Host compiler's command line of the Python entry of the target's operators."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch_dir = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
     return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
             "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
@@ -101,23 +108,33 @@ def up_to_date() -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Build both libraries (regular and checked) and the target operators' Python
-    entry, side by side, if one is missing or stale; return the regular library's path."""
+    entry, side by side, if one is missing or stale; return the regular library's path.
+    The libraries need nothing from Python: they are in place even where the entry's
+    compilation fails (which raises all the same)."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose else None
     jobs = []
     for lib, checked in ((LIB_PATH, False), (CHECKED_LIB_PATH, True)):
-        tmp = lib + f".tmp{os.getpid()}"
-        jobs.append((subprocess.Popen(compile_command(tmp, extra, checked)), tmp, lib))
-    if binding_path():
-        tmp = binding_path() + f".tmp{os.getpid()}"
-        jobs.append((subprocess.Popen(binding_command(tmp)), tmp, binding_path()))
+        built = lib + f".tmp{os.getpid()}"
+        jobs.append((subprocess.Popen(compile_command(built, extra, checked)), built, lib))
+    binding, entry = binding_path(), None
+    if binding:
+        tmp = binding + f".tmp{os.getpid()}"
+        entry = subprocess.Popen(binding_command(tmp))
     failed = [p.args for p, _, _ in jobs if p.wait() != 0]
+    entry_failed = entry is not None and entry.wait() != 0
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
-    for _, tmp, lib in jobs:
-        os.replace(tmp, lib)
+    for _, built, lib in jobs:
+        os.replace(built, lib)
+    if entry_failed:
+        if os.path.exists(binding):                      # an older one does not fit the new library
+            os.remove(binding)
+        raise subprocess.CalledProcessError(1, entry.args)
+    if binding:
+        os.replace(tmp, binding)
     return LIB_PATH
 
 
