@@ -14,8 +14,9 @@ statically, so the library loads on a machine without a GPU (its calls then
 fail with a CUDA error) and needs nothing from the Python environment.
 
 ``csrc/target_binding.cpp``, the Python entry of the target's operators, is compiled
-with the host compiler against the installed PyTorch's headers (its version is part
-of the file's name) and does not link against the library.
+with the host compiler against the installed PyTorch's and Python's headers (PyTorch's
+version and Python's ABI are part of the file's name) and does not link against the
+library.
 """
 from __future__ import annotations
 
@@ -80,7 +81,7 @@ def binding_path() -> str | None:
     torch_dir = _torch_dir()
     if torch_dir is None or not os.path.exists(os.path.join(torch_dir, "lib", "libc10_cuda.so")):
         return None
-    return os.path.join(BUILD_DIR, f"_target-{importlib.metadata.version('torch')}.so")
+    return os.path.join(BUILD_DIR, f"_target-{importlib.metadata.version('torch')}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def binding_command(out: str) -> list[str]:

@@ -5,6 +5,7 @@ import importlib.metadata
 import importlib.util
 import os
 import subprocess
+import sysconfig
 import types
 
 import pytest
@@ -70,3 +71,15 @@ def test_a_library_that_does_not_compile_replaces_nothing(build_dir, monkeypatch
     with pytest.raises(subprocess.CalledProcessError):
         lib_build.build(force=True)
     assert not os.path.exists(lib_build.LIB_PATH) and not os.path.exists(lib_build.binding_path())
+
+
+def test_the_entrys_name_tells_the_python_and_the_pytorch(build_dir, monkeypatch):
+    """Another Python in the same tree must not load what was built for this one."""
+    fake_torch(build_dir, monkeypatch, cuda=True)
+    mine = lib_build.binding_path()
+    var = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: {"EXT_SUFFIX": ".cpython-399-x.so"}.get(name, var(name)))
+    assert lib_build.binding_path() != mine and "9.9" in os.path.basename(mine)
+    lib_build.build(force=True)
+    monkeypatch.undo()
+    assert sysconfig.get_config_var("EXT_SUFFIX") in mine
