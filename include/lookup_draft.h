@@ -225,7 +225,10 @@ uint64_t lookup_draft_launch_count(void);
  * land (bounded again), marks its requests LOOKUP_DRAFT_LEN_FAILED and returns,
  * leaving the context usable.  Setting a tiny limit forces these paths, to test
  * them.  Process-wide; applies to launches made after the call.  0 restores the
- * default.
+ * default; more than 2^62 counts as 2^62.
+ * The same limit holds for each wait of lookup_draft_read_floor_bulk,
+ * lookup_paged_attention and lookup_verify_logits (lookup_target.h); the two latter
+ * return NaN and error rows when one runs out.
  */
 void lookup_draft_set_wait_limit_ns(uint64_t ns);
 

@@ -428,9 +428,11 @@ def read_floor(data, ctas_per_sm: int = 4, threads: int = 256, out=None, stream=
 
 
 def set_wait_limit_ns(ns: int) -> None:
-    """Diagnostics: limit on each bounded wait inside the scan and the bulk read
-    floor (0 = default 1 s)."""
-    load_library().lookup_draft_set_wait_limit_ns(int(ns))
+    """Diagnostics: limit on each bounded wait inside the scan, the bulk read floor,
+    lookup_paged_attention and lookup_verify_logits (0 = default 1 s).  Where one runs
+    out a drafting request is marked LEN_FAILED, attention returns NaN and verification
+    error rows."""
+    load_library().lookup_draft_set_wait_limit_ns(min(int(ns), (1 << 64) - 1))
 
 
 # ------------------------------------------------------------- loop steps ----

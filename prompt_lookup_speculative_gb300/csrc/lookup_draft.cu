@@ -94,6 +94,7 @@ constexpr int kLaneFillMinB = 1024;    // batches from this size use the lane-pe
 
 constexpr unsigned long long kKeyFailed = ~0ull;
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
+constexpr uint64_t kMostWaitNs = 1ull << 62;             // twice it, and it on top of the global timer, fit 64 bits
 
 static_assert(4 * kHaloQuads >= LOOKUP_DRAFT_MAX_M - 1, "halo too small for LOOKUP_DRAFT_MAX_M");
 
@@ -1762,7 +1763,7 @@ const char *lookup_draft_last_cuda_error(void) { return g_cuda_msg; }
 
 uint64_t lookup_draft_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
-void lookup_draft_set_wait_limit_ns(uint64_t ns) { g_wait_ns.store(ns ? ns : kDefaultWaitNs); }
+void lookup_draft_set_wait_limit_ns(uint64_t ns) { g_wait_ns.store(ns ? std::min(ns, kMostWaitNs) : kDefaultWaitNs); }
 
 int lookup_draft_plan(const int32_t *tokens, const int64_t *offsets, int32_t B, int32_t min_m, int32_t max_m,
                       const int32_t *model_draft, const int32_t *committed, int32_t H, int32_t T,

@@ -11,7 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pkg = pytest.importorskip("prompt_lookup_speculative_gb300")
 
-from test_gpu_target import BF16, F16, F32, attention_case, check_verify, gen, verify_case  # noqa: E402
+from test_gpu_target import BF16, F16, F32, attention_case, check_attention, check_verify, gen, verify_case  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -105,6 +105,24 @@ def test_attention_long_tail_behind_one_large_score(dt, gap, B, N, Hq, Hkv, D, L
         assert bool(((out[b].double() - o).abs() <= bound).all()), float(((out[b].double() - o).abs() / bound).max())
         one = (gap + z[..., 0].log()).repeat_interleave(Hq // Hkv, 0).T
         assert bool(((lse[b].double() - one).abs() <= one.abs() * 2.0 ** -22 + (L + 64) * 2.0 ** -24).all())
+
+
+# ------------------------------------------------------------- wait limits ----
+@pytest.mark.parametrize("ns", [1 << 62, 1 << 63, (1 << 63) + 1, (1 << 64) - 1, 1 << 70])
+def test_a_wait_limit_of_any_size_is_a_long_one(ns):
+    """Limits that would pass 64 bits once doubled, or on top of the timer."""
+    draft = [torch.tensor(x, device="cuda") for x in ([5, 6, 7, 8, 9, 5, 6, 7, 8], [0, 9])]
+    args = draft[0].to(torch.int32), draft[1].to(torch.int64)
+    want = pkg.lookup_draft(*args, min_m=2, max_m=4, K=4)
+    pkg.set_wait_limit_ns(ns)
+    try:
+        check_attention(*attention_case([300, 31], [4, 3], 4, 4, 2, 128, 16, BF16, 22))
+        check_verify(verify_case(5, 3, 3001, BF16, "point", 12), least=0.6)
+        got = pkg.lookup_draft(*args, min_m=2, max_m=4, K=4)
+        torch.cuda.synchronize()
+    finally:
+        pkg.set_wait_limit_ns(0)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 # ----------------------------------------------------------------- streams ----
