@@ -573,6 +573,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
             if (q) race(std::true_type());
             else race(std::false_type());
         }
+        __syncwarp();                                    // the cluster's barrier wants whole warps
         cluster_wait();
         best = cluster_best(best, warps[0], places[0], rank, p.cluster);
         if (best.key == 0.0f && row.m > -INFINITY) {
