@@ -947,7 +947,9 @@ def _target():
     takes from Python, which for these kernels would be longer than they run.
 
     With ``stream=`` the call runs on that stream, and so do the outputs and workspace that
-    it allocates; order that stream after what made the inputs, and yours after it."""
+    it allocates; order that stream after what made the inputs, and yours after it.  The
+    calls have no backward pass: an input that requires a gradient while gradients are
+    recorded is refused."""
     global _target_module
     if _target_module is None:
         import importlib.util

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -55,6 +56,15 @@ const char *words(at::ScalarType t) {
 const at::Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) refuse_type(std::string(name) + " must be a torch tensor");
     return THPVariable_Unpack(o);
+}
+
+// A tensor that results depend on.  The operators have no backward pass, so where a
+// gradient is being recorded it would be lost without a word.
+const at::Tensor &operand(PyObject *o, const char *name) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        refuse(std::string(name) + " requires a gradient, which this call does not give: call it under torch.no_grad()");
+    return t;
 }
 
 // The pointer of a contiguous tensor of this type, shape and device.
@@ -200,7 +210,8 @@ struct Paged {
 };
 Paged paged(PyObject *k_cache, PyObject *v_cache, PyObject *table, PyObject *kv_len, PyObject *q_len, int64_t B,
             int64_t D, at::ScalarType type, const c10::Device &dev) {
-    const at::Tensor &kc = tensor(k_cache, "k_cache"), &bt = tensor(table, "block_table");
+    const at::Tensor &kc = operand(k_cache, "k_cache"), &bt = tensor(table, "block_table");
+    operand(v_cache, "v_cache");
     if (kc.dim() != 4 || bt.dim() != 2)
         refuse("k_cache must be [pages, Hkv, page_size, D] and block_table [B, max_pages]");
     const int64_t shape[4] = {kc.size(0), kc.size(1), kc.size(2), D};
@@ -219,7 +230,7 @@ Paged paged(PyObject *k_cache, PyObject *v_cache, PyObject *table, PyObject *kv_
 
 PyObject *kv_append(PyObject *const *a, Py_ssize_t n) {
     expect(n, 13);
-    const at::Tensor &q = tensor(a[0], "q");
+    const at::Tensor &q = operand(a[0], "q");
     const c10::Device dev = cuda_device(q, "q");
     if (q.dim() != 4) refuse("q must be [B, N, Hq, D]");
     const int64_t B = q.size(0), N = q.size(1), hq = q.size(2), D = q.size(3);
@@ -228,8 +239,8 @@ PyObject *kv_append(PyObject *const *a, Py_ssize_t n) {
     const Paged c = paged(a[5], a[6], a[4], a[3], a[8], B, D, type, dev);
     int64_t qs[3], ks[3], vs[3];
     const void *qp = strided(q, "q", type, {B, N, hq, D}, dev, qs);
-    const void *kp = strided(tensor(a[1], "k"), "k", type, {B, N, int64_t(c.hkv), D}, dev, ks);
-    const void *vp = strided(tensor(a[2], "v"), "v", type, {B, N, int64_t(c.hkv), D}, dev, vs);
+    const void *kp = strided(operand(a[1], "k"), "k", type, {B, N, int64_t(c.hkv), D}, dev, ks);
+    const void *vp = strided(operand(a[2], "v"), "v", type, {B, N, int64_t(c.hkv), D}, dev, vs);
     const float *rotary = nullptr;
     int32_t max_pos = 0, rot = 0;
     if (a[7] != Py_None) {
@@ -257,7 +268,7 @@ PyObject *kv_append(PyObject *const *a, Py_ssize_t n) {
 
 PyObject *attention(PyObject *const *a, Py_ssize_t n) {
     expect(n, 12);
-    const at::Tensor &q = tensor(a[0], "q");
+    const at::Tensor &q = operand(a[0], "q");
     const c10::Device dev = cuda_device(q, "q");
     if (q.dim() != 4) refuse("q must be [B, N, Hq, D]");
     const int64_t B = q.size(0), N = q.size(1), hq = q.size(2), D = q.size(3);
@@ -285,7 +296,7 @@ PyObject *attention(PyObject *const *a, Py_ssize_t n) {
 
 PyObject *verify(PyObject *const *a, Py_ssize_t n) {
     expect(n, 14);
-    const at::Tensor &logits = tensor(a[2], "logits"), &block = tensor(a[0], "block");
+    const at::Tensor &logits = operand(a[2], "logits"), &block = tensor(a[0], "block");
     const c10::Device dev = cuda_device(logits, "logits");
     if (block.dim() != 2 || logits.dim() != 3) refuse("block must be [B, P] and logits [B, P + 1, V]");
     const int64_t B = block.size(0), P = block.size(1), V = logits.size(2);
@@ -296,7 +307,7 @@ PyObject *verify(PyObject *const *a, Py_ssize_t n) {
     const float *u = a[4] == Py_None && !noise ? nullptr : dense<float>(a[4], "u", at::kFloat, {B, P}, dev);
     const float *temperature = maybe<float>(a[5], "temperature", at::kFloat, {B}, dev);
     const void *qprobs =
-        a[6] == Py_None ? nullptr : strided(tensor(a[6], "qprobs"), "qprobs", at::kFloat, {B, P, V}, dev, qs);
+        a[6] == Py_None ? nullptr : strided(operand(a[6], "qprobs"), "qprobs", at::kFloat, {B, P, V}, dev, qs);
     const int32_t *point = maybe<int32_t>(a[7], "point_mass", at::kInt, {B, P}, dev);
     const int32_t *blk = dense<int32_t>(a[0], "block", at::kInt, {B, P}, dev);
     const int32_t *len = dense<int32_t>(a[1], "len", at::kInt, {B}, dev);

@@ -107,6 +107,38 @@ def test_attention_long_tail_behind_one_large_score(dt, gap, B, N, Hq, Hkv, D, L
         assert bool(((lse[b].double() - one).abs() <= one.abs() * 2.0 ** -22 + (L + 64) * 2.0 ** -24).all())
 
 
+# --------------------------------------------------------------- arguments ----
+def grad_calls():
+    """The three calls as functions of an input that requires a gradient, by its name."""
+    q, kc, vc, table, kv, ql = (x.cuda() for x in attention_case([30, 70], [4, 4], 4, 4, 2, 64, 16, BF16, 3))
+    c = {k: None if v is None else v.cuda() for k, v in verify_case(3, 2, 101, F32, "draft", 5).items()}
+
+    def attention(**x):
+        return pkg.lookup_paged_attention(*(x.get(n, t) for n, t in (("q", q), ("k_cache", kc), ("v_cache", vc))), table, kv)
+
+    def append(**x):
+        t = dict(q=q, k=q[:, :, :2], v=q[:, :, 2:]) | x
+        return pkg.lookup_kv_append(t["q"], t["k"], t["v"], kv, table, kc, vc)
+
+    def verify(**x):
+        t = c | x
+        return pkg.lookup_verify_logits(t["block"], t["length"], t["logits"], noise=t["noise"], u=t["u"], qprobs=t["qprobs"])
+
+    return [(attention, "q", q), (attention, "k_cache", kc), (attention, "v_cache", vc), (append, "q", q),
+            (append, "k", q[:, :, :2]), (append, "v", q[:, :, 2:]), (verify, "logits", c["logits"]), (verify, "qprobs", c["qprobs"])]
+
+
+def test_a_gradient_that_would_be_lost_is_refused():
+    for call, name, x in grad_calls():
+        x = x.clone().requires_grad_()
+        with pytest.raises(ValueError, match=f"{name} requires a gradient"):
+            call(**{name: x})
+        with torch.no_grad():
+            got = call(**{name: x})
+        want = call(**{name: x.detach()})
+        assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
+
+
 # ------------------------------------------------------------- wait limits ----
 @pytest.mark.parametrize("ns", [1 << 62, 1 << 63, (1 << 63) + 1, (1 << 64) - 1, 1 << 70])
 def test_a_wait_limit_of_any_size_is_a_long_one(ns):
