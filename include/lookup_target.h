@@ -108,8 +108,8 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
  * A call whose bounded waits run out on the device (lookup_draft_set_wait_limit_ns)
  * returns NaN in every element of out and lse.
  * Errors: LOOKUP_DRAFT_EINVAL for sizes outside their ranges, a null pointer other than
- * q_len and lse, pointers or strides of q and the caches that are not multiples of 16 bytes, a
- * workspace that is too small, or caches (pages * Hkv * page_size) or block tables
+ * q_len and lse, pointers of q, the caches, out and the workspace or strides of q's axes of two
+ * or more that are not multiples of 16 bytes, B * N * Hq above 2^30, a workspace that is too small, or caches (pages * Hkv * page_size) or block tables
  * (max_pages * page_size) of 2^31 - 129 rows or more.
  */
 size_t lookup_paged_attention_workspace_bytes(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);

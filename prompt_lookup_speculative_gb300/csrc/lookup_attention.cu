@@ -1386,8 +1386,9 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
         return LOOKUP_DRAFT_EINVAL;
     for (const void *x : {q, k_cache, v_cache, static_cast<const void *>(workspace), static_cast<const void *>(out)})
         if (misaligned(x, 16)) return LOOKUP_DRAFT_EINVAL;
-    for (int k = 0; k < 3; ++k)
-        if (q_strides[k] & 7) return LOOKUP_DRAFT_EINVAL;
+    const int64_t axes[3] = {B, N, Hq};
+    for (int k = 0; k < 3; ++k)                              // (an axis of one has any stride: it is not used)
+        if (axes[k] > 1 && (q_strides[k] & 7)) return LOOKUP_DRAFT_EINVAL;
     if (misaligned(block_table, 4) || misaligned(kv_len, 4) || misaligned(q_len, 4) || misaligned(lse, 4))
         return LOOKUP_DRAFT_EINVAL;
     const int G = Hq / Hkv;

@@ -290,9 +290,12 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
         if (misaligned(x, 4)) return LOOKUP_DRAFT_EINVAL;
     Params p{};
     p.q = q, p.k = k, p.v = v;
-    if (q) p.qs = Strides{q_strides[0], q_strides[1], q_strides[2]};
-    if (k) p.ks = Strides{k_strides[0], k_strides[1], k_strides[2]};
-    if (v) p.vs = Strides{v_strides[0], v_strides[1], v_strides[2]};
+    auto strides = [&](const int64_t *s, int32_t heads) {    // an axis of one has any: it is not used
+        return Strides{B > 1 ? s[0] : 0, N > 1 ? s[1] : 0, heads > 1 ? s[2] : 0};
+    };
+    if (q) p.qs = strides(q_strides, Hq);
+    if (k) p.ks = strides(k_strides, Hkv);
+    if (v) p.vs = strides(v_strides, Hkv);
     p.kv_len = kv_len, p.q_len = q_len, p.table = block_table, p.rotary = rotary;
     p.k_cache = k_cache, p.v_cache = v_cache, p.out_q = out_q, p.status = status;
     p.B = B, p.N = N, p.Hq = Hq, p.Hkv = Hkv, p.D = D, p.max_pages = max_pages, p.pages = pages;

@@ -139,6 +139,23 @@ def test_a_gradient_that_would_be_lost_is_refused():
         assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("B,N,Hq", [(1, 3, 4), (3, 1, 4), (3, 4, 1), (1, 1, 1)])
+def test_an_axis_of_one_may_have_any_stride(B, N, Hq):
+    """PyTorch leaves such strides as they come out, and nothing is read by them."""
+    q, kc, vc, table, kv, ql = (x.cuda() for x in attention_case([33, 70, 5][:B], [N] * B, N, Hq, 1, 64, 16, BF16, 6))
+    odd = q.as_strided(q.shape, [s if n > 1 else 515 for n, s in zip(q.shape[:3], q.stride())] + [1])
+    want = pkg.lookup_paged_attention(q, kc, vc, table, kv)
+    got = pkg.lookup_paged_attention(odd, kc, vc, table, kv)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    kv0 = q[:, :, :1].contiguous()
+    odd_kv = kv0.as_strided(kv0.shape, [s if n > 1 else 515 for n, s in zip(kv0.shape[:3], kv0.stride())] + [1])
+    caches = [(kc.clone(), vc.clone()) for _ in range(2)]
+    want = pkg.lookup_kv_append(q, kv0, kv0, kv, table, *caches[0])
+    got = pkg.lookup_kv_append(odd, odd_kv, odd_kv, kv, table, *caches[1])
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(*caches))
+
+
 # ------------------------------------------------------------- wait limits ----
 @pytest.mark.parametrize("ns", [1 << 62, 1 << 63, (1 << 63) + 1, (1 << 64) - 1, 1 << 70])
 def test_a_wait_limit_of_any_size_is_a_long_one(ns):
