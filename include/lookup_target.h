@@ -136,7 +136,7 @@ int lookup_paged_attention(const void *q, const int64_t *q_strides, const void *
  * noise         float [B][V], exponential draws (> 0), or NULL: every request greedy
  * temperature   float [B] or NULL (= 1): a request whose value is not a positive
  *               finite number is greedy
- * u             float [B][P], uniform [0, 1) draws (needed with noise)
+ * u             float [B][P], uniform [0, 1) draws (needed with noise where P > 0)
  * qprobs        float [B][P][V] or NULL: the proposal distribution at each position,
  *               the last axis dense, strides in elements; NULL = every position is
  *               a point mass

@@ -304,7 +304,7 @@ PyObject *verify(PyObject *const *a, Py_ssize_t n) {
     int64_t ls[2], qs[2] = {0, 0};
     const void *lp = strided(logits, "logits", logits.scalar_type(), {B, P + 1, V}, dev, ls);
     const float *noise = maybe<float>(a[3], "noise", at::kFloat, {B, V}, dev);
-    const float *u = a[4] == Py_None && !noise ? nullptr : dense<float>(a[4], "u", at::kFloat, {B, P}, dev);
+    const float *u = a[4] == Py_None && (!noise || P == 0) ? nullptr : dense<float>(a[4], "u", at::kFloat, {B, P}, dev);
     const float *temperature = maybe<float>(a[5], "temperature", at::kFloat, {B}, dev);
     const void *qprobs =
         a[6] == Py_None ? nullptr : strided(operand(a[6], "qprobs"), "qprobs", at::kFloat, {B, P, V}, dev, qs);

@@ -156,6 +156,15 @@ def test_an_axis_of_one_may_have_any_stride(B, N, Hq):
     assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(*caches))
 
 
+def test_sampling_without_proposals_needs_no_uniforms():
+    """P = 0 is plain sampling: noise alone decides."""
+    c = verify_case(7, 0, 777, BF16, "point", 9)
+    want = check_verify(c)
+    got = pkg.lookup_verify_logits(c["block"].cuda(), c["length"].cuda(), c["logits"].cuda(), noise=c["noise"].cuda(),
+                                   temperature=c["temperature"].cuda())
+    assert all(torch.equal(x.cpu(), y) for x, y in zip(got, want))
+
+
 # ------------------------------------------------------------- wait limits ----
 @pytest.mark.parametrize("ns", [1 << 62, 1 << 63, (1 << 63) + 1, (1 << 64) - 1, 1 << 70])
 def test_a_wait_limit_of_any_size_is_a_long_one(ns):
