@@ -94,7 +94,6 @@ constexpr int kLaneFillMinB = 1024;    // batches from this size use the lane-pe
 
 constexpr unsigned long long kKeyFailed = ~0ull;
 constexpr uint64_t kDefaultWaitNs = 1000000000ull;
-constexpr uint64_t kMostWaitNs = 1ull << 62;             // twice it, and it on top of the global timer, fit 64 bits
 
 static_assert(4 * kHaloQuads >= LOOKUP_DRAFT_MAX_M - 1, "halo too small for LOOKUP_DRAFT_MAX_M");
 
@@ -1160,6 +1159,7 @@ int cuda_fail(cudaError_t e, const char *what) {
         if (e_ != cudaSuccess) return cuda_fail(e_, #call); \
     } while (0)
 
+constexpr uint64_t kMostWaitNs = 1ull << 62;             // twice it, and it on top of the global timer, fit 64 bits
 std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};
 
 // The device address of page-locked host memory the device can address, else
