@@ -107,6 +107,10 @@ int lookup_kv_append(const void *q, const int64_t *q_strides, const void *k, con
  * (the block's own tokens, a window's edge), may reach the others.
  * A call whose bounded waits run out on the device (lookup_draft_set_wait_limit_ns)
  * returns NaN in every element of out and lse.
+ * Made for blocks of N * Hq / Hkv <= 128 rows, a verify block or one token.  A longer
+ * block (a prompt) is right, but every 128 rows of it go through all the positions
+ * that any of its tokens sees: twice the work where nothing was cached before it, and
+ * the whole length where the window is short.
  * Errors: LOOKUP_DRAFT_EINVAL for sizes outside their ranges, a null pointer other than
  * q_len and lse, pointers of q, the caches, out and the workspace or strides of q's axes of two
  * or more that are not multiples of 16 bytes, B * N * Hq above 2^30, a workspace that is too small, or caches (pages * Hkv * page_size) or block tables

@@ -13,10 +13,13 @@
 // all their 16-byte loads are in flight together.  The last CTAs report the requests with
 // tokens that have no slot.  4 prompts of 8191 tokens, 32 query and 8 key-value heads of
 // 128: 138 us (5.6 TB/s, 83% of a copy's rate); 64 blocks of 16 tokens 5.0 us, one token
-// 2.3 us, which is the launch.
+// 2.3 us, which is the launch.  4096 blocks of 8 with 16 and 2 heads of 64 37 us (4.4 TB/s),
+// whatever the layout of the pairs, the rotated part and the head's size; as four prompts
+// 34 us: 7 us of start and end, then 5.9 TB/s, and the blocks' short runs of tokens.
 //
-// Sizes, strides or addresses that are not multiples of 16 bytes take a kernel of one pair
-// of elements per thread: right for every case, and 792 us for those prompts.
+// A head or a rotated part that is no multiple of 16 elements, and strides or addresses that
+// are no multiples of 16 bytes, take a kernel of one pair of elements per thread: right for
+// every case, and five to six times slower (796 us for those prompts, 183 for the blocks).
 
 #include "lookup_draft.h"
 #include "lookup_target.h"

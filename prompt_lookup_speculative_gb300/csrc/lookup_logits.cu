@@ -23,8 +23,8 @@
 // 64 blocks of 16 over 151936 bf16 logits: 56 us for 272 MB (4.9 TB/s, 72% of a copy's
 // rate), 43 of them the streaming and 13 the draws, which wait for the first kernel's
 // last row and then for a row and its noise.  64 blocks of 8 with a draft distribution
-// over float32 logits 58 us (5.3 TB/s), 8 blocks of 16 over 32000 logits 11.4 us, one
-// greedy block 5.6 us: there both kernels are latency.
+// over float32 logits 58 us (5.3 TB/s).  8 blocks of 16 over 32000 logits 11.3 us, 8.0 of
+// them without the race; one block 8.8, and 5.9 without: there both kernels are latency.
 
 #include "lookup_draft.h"
 #include "lookup_target.h"
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
 }
 
 // Segments of a row of `size`-byte logits: a tile each while there are fewer tiles than
-// warps, kSegTiles tiles at most.
+// warps (on a GB300's 152 SMs), kSegTiles tiles at most.
 int64_t segments(int32_t B, int32_t P, int32_t V, int size) {
     const int64_t tiles = (int64_t(V) * size / 16 + 2 + kTile - 1) / kTile;          // of a row
     const int64_t each = std::min<int64_t>(std::max<int64_t>(tiles * B * (P + 1) / (152 * kStatWarps), 1), kSegTiles);
@@ -621,7 +621,7 @@ int64_t segments(int32_t B, int32_t P, int32_t V, int size) {
 }
 
 // CTAs of a request's cluster: a power of two, one per 4096 logits of its race as
-// long as all clusters run at once (two CTAs per SM).  64 requests with 4 CTAs each take
+// long as all clusters run at once (304: two CTAs per SM).  64 requests with 4 CTAs each take
 // 56 us in all, with 1 83 us, with 8 62; 8 requests over 32000 logits 11.5 us with 8, 17 with 1.
 int cluster_for(int32_t B, int32_t V) {
     int c = 1;

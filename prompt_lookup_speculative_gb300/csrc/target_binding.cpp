@@ -1,7 +1,7 @@
 // target_binding.cpp -- Python entry of the target's operators (include/lookup_target.h).
 //
 // These calls take a dozen tensors each and their kernels run for microseconds: checked
-// and marshalled in Python they take 25 to 35 us to enqueue, here 6 to 10.  Everything a
+// and marshalled in Python they take 25 to 35 us to enqueue, here 5 to 12.  Everything a
 // call does is one function: check the tensors, allocate what the caller did not give,
 // enter the library through the C ABI (its entry points are handed over as addresses,
 // so nothing links against it) with the interpreter's lock released.  A function
