@@ -244,6 +244,26 @@ def test_an_output_released_early_is_not_used_again():
     assert torch.equal(kept, want)
 
 
+@pytest.mark.parametrize("name", ["attention", "verify", "append"])
+def test_a_graph_with_a_second_stream(name):
+    """A capture that forks to another stream for the call: the outputs are the graph's."""
+    side = torch.cuda.Stream()
+    call, want = calls_on(side)[name], calls_on(None)[name]()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = call()
+        here.wait_stream(side)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_a_stream_of_another_device_is_refused():
     class Elsewhere:
         stream_id, device_index, device_type = 0, 1, 1
