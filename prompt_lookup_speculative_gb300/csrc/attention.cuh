@@ -1100,7 +1100,9 @@ __global__ void __launch_bounds__(Shape<D, GROUPS>::kThreads, Shape<D, GROUPS>::
                 break;
             }
             tc_fence_after();
-            if (TREE && *const_cast<volatile uint32_t *>(&hd.odd) && warp_live) {
+            // (a thread of the other group may set the word just now: one answer for the warp, whose
+            // threads load and store tensor memory together)
+            if (TREE && warp_live && __any_sync(0xffffffffu, *const_cast<volatile uint32_t *>(&hd.odd) != 0)) {
 #pragma unroll 1
                 for (int j = 0; j < D; j += 32) {
                     uint32_t o[32];

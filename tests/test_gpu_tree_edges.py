@@ -1,0 +1,71 @@
+"""A verify step over a tree (include/lookup_tree.h), where it can go wrong: values of V that
+are not finite in many items at once, and visible ones of the smallest weights."""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pkg = pytest.importorskip("prompt_lookup_speculative_gb300")
+
+import tree_reference as ref  # noqa: E402
+from test_gpu_target import BF16, F16, close, gen  # noqa: E402
+from test_gpu_tree import tree_case  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def put(vc, table, at, col, value):
+    """One element of position `at`'s row of V, in every key-value head."""
+    page = vc.shape[2]
+    vc[table[at // page], :, at % page, col] = value
+
+
+def check_odd(case, places, scale=None, window=0, again=1):
+    """`places`: {request: [(node, column, value)]}, each value infinite or NaN.  What sees one
+    is that value in its column (NaN where it sees infinities of both signs), what does not is as
+    if it were not there."""
+    q, kc, vc, table, kv, ql, mask = case
+    B, N, Hq, D = q.shape
+    scale = D ** -0.5 if scale is None else scale
+    v1 = vc.clone()
+    want = ref.attention(q, kc, vc, table, kv, ql, mask, scale, window)
+    odd = torch.zeros((B, N, 1, D), dtype=torch.float64)
+    for r, some in places.items():
+        n, count = int(kv[r]), int(ql[r])
+        for (node, col), value in {(node, col): value for node, col, value in some}.items():     # (the last one stands)
+            put(v1, table[r], n + node, col, value)
+            for i in range(count):
+                if n + node in ref.seen(mask[r, i], n, count, n + count, window):
+                    odd[r, i, 0, col] += value
+    odd = odd.expand(-1, -1, Hq, -1)
+    hit = odd != 0                                       # (NaN is not 0 either)
+    assert bool(hit.any()) and not bool(hit.all())
+    d = [x.cuda() for x in (q, kc, v1, table, kv, mask, ql)]
+    first = None
+    for _ in range(again):
+        out, lse = pkg.lookup_tree_attention(*d[:6], q_len=d[6], scale=scale, window=window)
+        got = out.double().cpu()
+        assert bool(((got == odd) | (got.isnan() & odd.isnan()))[hit].all())
+        close(torch.where(hit, want[0], got), want[0], want[2], "out")
+        close(lse, want[1], want[3], "lse")
+        assert first is None or torch.equal(first.view(torch.int16), out.view(torch.int16))
+        first = out
+    return v1
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(64, 4, 1, 128), (40, 8, 2, 64), (20, 14, 2, 64), (12, 4, 1, 128), (5, 8, 1, 128)])
+def test_values_that_are_not_finite_in_some_of_many_items(N, Hq, Hkv, D):
+    """Both groups of a CTA look through the same tiles, item after item, some with such values
+    and some without: the same result, to the last bit, time after time."""
+    g = gen(N + D)
+    lens = [(37 * r * r) % 230 for r in range(400 // N)] * 4
+    qn = [N if r % 4 else max(2, N // 2) for r in range(len(lens))]
+    case = tree_case(lens, qn, N, Hq, Hkv, D, 16, BF16, N)
+    places = {}
+    for r in range(0, len(lens), 3):
+        values = [math.inf, -math.inf, math.nan]
+        places[r] = [(int(torch.randint(qn[r], (1,), generator=g)), int(torch.randint(D, (1,), generator=g)),
+                      values[(r + k) % 3]) for k in range(2)]
+    check_odd(case, places, again=4)
