@@ -106,9 +106,11 @@ int lookup_norm_append(const void *q, const int64_t *q_strides, const void *k, c
  *
  * Token i < q_len[r] sees every cached position j < kv_len[r], and position kv_len[r] + j
  * where bit j of its mask is set.  A token that sees nothing has out = 0 and
- * lse = -infinity.  A value in v_cache that is not finite, in a slot of the block,
- * reaches the tokens that see it and no others (one in a slot before the block that
- * `window` hides from some tokens and not from others may reach those).
+ * lse = -infinity.  A value in v_cache that is not finite reaches every token that sees
+ * it, however small its weight: that element of out is infinite or NaN.  In a slot of the
+ * block it reaches no others, and as the weighted sum has it (an infinity stays one); in a
+ * slot before the block that `window` hides from some tokens and not from others it may
+ * reach those.
  * For a given request, N, D and head counts the sums are added in an order that depends
  * on the whole batch's lengths: the same call gives the same bits every time.
  * Blocks of more than 128 rows (N * Hq / Hkv) of D = 64 or 128 go through the cache once

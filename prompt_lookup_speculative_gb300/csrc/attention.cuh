@@ -82,6 +82,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -534,9 +535,13 @@ __device__ inline uint32_t finite_part(uint32_t w) {
     return w;
 }
 
+// What is not finite of a sum whose factor is 0: a weight that is too small for float32 is
+// still above 0, so an infinity or NaN stays.
+__device__ inline float odd_part(float x) { return fabsf(x) <= FLT_MAX ? 0.0f : x; }
+
 // Values of V that are not finite and that this thread's row sees in the tiles of its part,
-// added to its 32 columns of O from j on (their weights are positive).  A thread's row is one
-// of the request's; the rows of V come from the cache.
+// added to its 32 columns of O from j on: whatever their weights are, as these are above 0.
+// A thread's row is one of the request's; the rows of V come from the cache.
 template <typename T, int D, typename S>
 __device__ __noinline__ void add_odd(const Params &p, int r, int h, int i, int a, int b, int j, uint32_t (&o)[32]) {
     const Request q = request_of<S, true>(p, r);
@@ -1015,7 +1020,8 @@ __global__ void __launch_bounds__(Shape<D, GROUPS>::kThreads, Shape<D, GROUPS>::
                             tc_wait_ld(o);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                o[k] = __float_as_uint(f == 0.0f ? 0.0f : __uint_as_float(o[k]) * f);
+                                o[k] = __float_as_uint(f != 0.0f ? __uint_as_float(o[k]) * f
+                                                       : TREE ? odd_part(__uint_as_float(o[k])) : 0.0f);
                             tc_st(tmem + lanes + S::kO + j, o);
                         }
                     }
@@ -1134,7 +1140,8 @@ __global__ void __launch_bounds__(Shape<D, GROUPS>::kThreads, Shape<D, GROUPS>::
                                 uint32_t v[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    v[e] = f == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[4 * k + e]) * f);
+                                    v[e] = __float_as_uint(f != 0.0f ? __uint_as_float(o[4 * k + e]) * f
+                                                           : TREE ? odd_part(__uint_as_float(o[4 * k + e])) : 0.0f);
                                 *reinterpret_cast<uint4 *>(stage + y * (kRows * 128) + lane * 128 +
                                                            ((k ^ (lane & 7)) << 4)) =
                                     make_uint4(v[0], v[1], v[2], v[3]);
@@ -1290,7 +1297,7 @@ struct JoinSmem {
 // ROWS rows at a time, first their weights 2^(c (m_k - M)), a warp per row and a lane
 // per part; then each warp sums every eighth part over those rows, and the warps' sums
 // are added.
-template <typename T, int D, int ROWS, int GROUPS>
+template <typename T, int D, int ROWS, int GROUPS, bool TREE>
 __device__ void join_item(const Params &p, int c, int g, const Meta &meta, JoinSmem<D, ROWS, GROUPS> &sm) {
     constexpr int E = D / 32;                            // columns of a lane
     constexpr int kFirst = 512 / D / ROWS > 0 ? 512 / D / ROWS * (D == 256 ? 1 : 2) : 1;     // parts of a warp in flight
@@ -1338,12 +1345,12 @@ __device__ void join_item(const Params &p, int c, int g, const Meta &meta, JoinS
 #pragma unroll
                 for (int k = 0; k < kFewParts; ++k) {
                     const float w = s[y][k] == 0.0f ? 0.0f : m[y][k] == big ? 1.0f : exp2f((m[y][k] - big) * p.c);
-                    if (w == 0.0f) continue;
-                    sum += w * s[y][k];
+                    if (TREE ? s[y][k] == 0.0f : w == 0.0f) continue;
+                    if (w != 0.0f) sum += w * s[y][k];
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e) {
-                        o[2 * e] += w * v[y][k][e].x;
-                        o[2 * e + 1] += w * v[y][k][e].y;
+                        o[2 * e] += TREE && w == 0.0f ? odd_part(v[y][k][e].x) : w * v[y][k][e].x;
+                        o[2 * e + 1] += TREE && w == 0.0f ? odd_part(v[y][k][e].y) : w * v[y][k][e].y;
                     }
                 }
                 finish(row0 + y * step, o, big, sum);
@@ -1401,8 +1408,8 @@ __device__ void join_item(const Params &p, int c, int g, const Meta &meta, JoinS
                     const float w = y < rows ? sm.weights[y][at] : 0.0f;
 #pragma unroll
                     for (int e = 0; e < E / 2; ++e) {
-                        o[y][2 * e] += w == 0.0f ? 0.0f : w * v[f][y][e].x;
-                        o[y][2 * e + 1] += w == 0.0f ? 0.0f : w * v[f][y][e].y;
+                        o[y][2 * e] += w != 0.0f ? w * v[f][y][e].x : TREE ? odd_part(v[f][y][e].x) : 0.0f;
+                        o[y][2 * e + 1] += w != 0.0f ? w * v[f][y][e].y : TREE ? odd_part(v[f][y][e].y) : 0.0f;
                     }
                 }
             }
@@ -1429,7 +1436,7 @@ __device__ void join_item(const Params &p, int c, int g, const Meta &meta, JoinS
 
 // The items that were cut: CTA x takes those begun by CTAs (and groups) x, x + gridDim.x, ... of
 // attention_kernel.  A wait that ran out anywhere makes the whole call's rows NaN.
-template <typename T, int D, int ROWS, int GROUPS>
+template <typename T, int D, int ROWS, int GROUPS, bool TREE>
 __global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 3) join_kernel(const __grid_constant__ Params p) {
     __shared__ JoinSmem<D, ROWS, GROUPS> sm;
     wait_for_prerequisite_grid();
@@ -1451,7 +1458,7 @@ __global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 3) join_kernel(co
         return;
     }
     for (int c = blockIdx.x, k = 0; c < p.ctas * GROUPS; c += gridDim.x, ++k)
-        if (sm.metas[k].r >= 0) join_item<T, D, ROWS, GROUPS>(p, c / GROUPS, c % GROUPS, sm.metas[k], sm);
+        if (sm.metas[k].r >= 0) join_item<T, D, ROWS, GROUPS, TREE>(p, c / GROUPS, c % GROUPS, sm.metas[k], sm);
 }
 
 // -------------------------------------------------------------------- host ----
@@ -1552,7 +1559,7 @@ int launch(Params &p, cudaStream_t stream) {
     cfg.gridDim = dim3(unsigned(over), per);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    r = cudaLaunchKernelEx(&cfg, single ? join_kernel<T, D, 1, GROUPS> : join_kernel<T, D, 4, GROUPS>, p);
+    r = cudaLaunchKernelEx(&cfg, single ? join_kernel<T, D, 1, GROUPS, TREE> : join_kernel<T, D, 4, GROUPS, TREE>, p);
     if (r != cudaSuccess) return cuda_fail(r, "kernel launch");
     lookup_note_launch();
     return LOOKUP_DRAFT_OK;

@@ -69,3 +69,52 @@ def test_values_that_are_not_finite_in_some_of_many_items(N, Hq, Hkv, D):
         places[r] = [(int(torch.randint(qn[r], (1,), generator=g)), int(torch.randint(D, (1,), generator=g)),
                       values[(r + k) % 3]) for k in range(2)]
     check_odd(case, places, again=4)
+
+
+SHAPES = [(5, 4, 1, 128), (12, 4, 1, 128), (30, 4, 1, 128), (64, 4, 1, 128), (7, 4, 1, 64), (40, 8, 2, 64), (9, 4, 2, 256)]
+
+
+@pytest.mark.parametrize("lens", [[6000, 3000], [0, 3, 20, 9] * 80, [700, 90, 1500, 2, 300, 1100] * 6])
+@pytest.mark.parametrize("N,Hq,Hkv,D", SHAPES)
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_values_that_are_not_finite_reach_those_of_the_smallest_weights(dt, N, Hq, Hkv, D, lens):
+    """Scores hundreds apart, so that most weights vanish in float32: an infinity that is seen
+    with one of them is still one, in an item of many parts, of one, and of a few."""
+    rows = 600 // N
+    lens = lens if len(lens) < 40 else lens[:max(rows, 8)]
+    qn = [N - r % 3 for r in range(len(lens))]
+    case = tree_case(lens, qn, N, Hq, Hkv, D, 16, dt, N + len(lens))
+    q, kc, _, table, _, _, mask = case
+    places = {r: [(1 + r % 2, 5 + r % 40, math.inf), (N // 2, 60 - r % 9, -math.inf)] for r in range(0, len(lens), 2)}
+    least = 0.0
+    for r in places:                                     # the smallest weight that counts, of head 0
+        n = lens[r]
+        for row in range(qn[r]):
+            at = ref.seen(mask[r, row], n, qn[r], n + qn[r], 0)
+            hits = [at.index(n + node) for node, _, _ in places[r] if n + node in at]
+            if hits:
+                k = torch.stack([kc[table[r, x // 16], 0, x % 16] for x in at]).double()
+                z = 20.0 * (k @ q[r, row, 0].double())
+                least = min(least, float((z[hits] - z.max()).min()))
+    assert least < -150.0
+    check_odd(case, places, scale=20.0)
+
+
+@pytest.mark.parametrize("lens", [[6000, 3000], [200, 330, 190, 140]])
+@pytest.mark.parametrize("N,Hq,Hkv,D", SHAPES)
+def test_cached_values_that_are_not_finite_reach_all_that_see_them(N, Hq, Hkv, D, lens):
+    """In positions that every token sees: infinite or NaN, whatever the weight, and nothing else
+    changes."""
+    case = tree_case(lens, [N] * len(lens), N, Hq, Hkv, D, 16, BF16, N + len(lens))
+    q, kc, vc, table, kv, ql, mask = case
+    v1 = vc.clone()
+    for r, n in enumerate(lens):
+        put(v1, table[r], 3 + 7 * r, 9, math.inf)
+        put(v1, table[r], n // 2, 33, -math.inf)
+    want = ref.attention(q, kc, vc, table, kv, ql, mask, 20.0, 0)
+    out, lse = pkg.lookup_tree_attention(*(x.cuda() for x in (q, kc, v1, table, kv, mask)), scale=20.0)
+    got = out.double().cpu()
+    assert not bool(got[..., [9, 33]].isfinite().any())
+    got[..., [9, 33]] = want[0][..., [9, 33]]
+    close(got, want[0], want[2], "out")
+    close(lse, want[1], want[3], "lse")
