@@ -1020,8 +1020,8 @@ __global__ void __launch_bounds__(Shape<D, GROUPS>::kThreads, Shape<D, GROUPS>::
                             tc_wait_ld(o);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                o[k] = __float_as_uint(f != 0.0f ? __uint_as_float(o[k]) * f
-                                                       : TREE ? odd_part(__uint_as_float(o[k])) : 0.0f);
+                                // (trees: 0 times what is not finite is NaN, and that reaches the row)
+                                o[k] = __float_as_uint(!TREE && f == 0.0f ? 0.0f : __uint_as_float(o[k]) * f);
                             tc_st(tmem + lanes + S::kO + j, o);
                         }
                     }
