@@ -423,7 +423,8 @@ template <typename S>
 struct Head {
     uint64_t full[16], empty[16];        // slots
     GroupBars groups[S::kGroups];
-    uint32_t tmem, failed, odd;          // odd: a value of V was not finite (trees; it stays set)
+    uint32_t tmem, failed;
+    uint32_t odd;                        // trees: the last item, from 1 on, in which a value of V was not finite
     int32_t start_r;
     int64_t start_off, total;
     int64_t warp_sum[S::kThreads / 32];
@@ -947,7 +948,7 @@ __global__ void __launch_bounds__(Shape<D, GROUPS>::kThreads, Shape<D, GROUPS>::
                             const uint4 w = *piece;
                             if (not_finite(w.x, T()) || not_finite(w.y, T()) || not_finite(w.z, T()) || not_finite(w.w, T())) {
                                 // (the other group may find zeros here already: the word first)
-                                *const_cast<volatile uint32_t *>(&hd.odd) = 1;
+                                atomicMax(&hd.odd, item + 1);
                                 __threadfence_block();
                                 *piece = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
                             }
@@ -1106,9 +1107,9 @@ __global__ void __launch_bounds__(Shape<D, GROUPS>::kThreads, Shape<D, GROUPS>::
                 break;
             }
             tc_fence_after();
-            // (a thread of the other group may set the word just now: one answer for the warp, whose
-            // threads load and store tensor memory together)
-            if (TREE && warp_live && __any_sync(0xffffffffu, *const_cast<volatile uint32_t *>(&hd.odd) != 0)) {
+            // (a thread of the other group, further on, may set the word just now: one answer for the
+            // warp, whose threads load and store tensor memory together; to look for nothing is right too)
+            if (TREE && warp_live && __any_sync(0xffffffffu, *const_cast<volatile uint32_t *>(&hd.odd) > item)) {
 #pragma unroll 1
                 for (int j = 0; j < D; j += 32) {
                     uint32_t o[32];
