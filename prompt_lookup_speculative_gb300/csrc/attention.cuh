@@ -946,12 +946,17 @@ __global__ void __launch_bounds__(Shape<D, GROUPS>::kThreads, Shape<D, GROUPS>::
                             *piece = make_uint4(0, 0, 0, 0);
                         } else if (TREE) {
                             const uint4 w = *piece;
-                            if (not_finite(w.x, T()) || not_finite(w.y, T()) || not_finite(w.z, T()) || not_finite(w.w, T())) {
-                                // (the other group may find zeros here already: the word first)
+                            bool odd = not_finite(w.x, T()) || not_finite(w.y, T()) || not_finite(w.z, T()) ||
+                                       not_finite(w.w, T());
+                            if (odd) {                   // (the other group may find zeros here already: the word first)
                                 atomicMax(&hd.odd, item + 1);
                                 __threadfence_block();
-                                *piece = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
+                            } else if (GROUPS > 1) {     // what the other one stored, stored again: ahead of this group's
+                                __threadfence_block();   // own fence and product
+                                odd = *const_cast<volatile uint32_t *>(&hd.odd) > item;
                             }
+                            if (odd)
+                                *piece = make_uint4(finite_part<T>(w.x), finite_part<T>(w.y), finite_part<T>(w.z), finite_part<T>(w.w));
                         }
                     }
                     if (TREE) __threadfence_block();
