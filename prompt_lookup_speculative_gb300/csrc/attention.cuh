@@ -65,9 +65,9 @@
 // would read the cache once more.  So one CTA per SM has two groups, each with a row tile,
 // its own four softmax warps, product warp and half of tensor memory; they share the loads
 // and the ring of K and V tiles, which a slot leaves when both groups' products are over.
-// 32 trees of 64 nodes over 25000 positions, 32 heads on 8 at D = 128: 908 us (3.7 TB/s);
-// 16 of 25 over 512 to 131072, 14 heads on 2 at D = 64: 111 us; one of 15 over 4096: 25 us
-// as called.
+// 32 trees of 64 nodes over 25000 positions, 32 heads on 8 at D = 128: 918 us (3.6 TB/s);
+// 16 of 25 over 512 to 131072, 14 heads on 2 at D = 64: 110 us; one of 15 over 4096, one
+// group: 24 us.
 #pragma once
 
 #include "lookup_draft.h"
@@ -1471,7 +1471,15 @@ __global__ void __launch_bounds__(kJoinThreads, D == 256 ? 2 : 3) join_kernel(co
 int cuda_fail(cudaError_t e, const char *what) { return lookup_record_cuda_error(e, what); }
 
 // Row tiles of a CTA at a time: two for a tree that has more than one, where both fit tensor
-// memory.
+// memory.  With two, and with one and two CTAs per SM, us: at D = 128, 32 heads on 8, 32 trees
+// of 64 nodes over 25000 positions 916 and 989, of 33 nodes 774 and 959; 64 of 48 over 4000 321
+// and 356; 256 of 40 over 500, 16 heads on 4, 144 and 174; one of 64 over 4096 26.6 and 25.6.
+// At D = 64 the second CTA is worth about as much as the shared loads: those 694 and 682, 633
+// and 638, 250 and 250, 133 and 134, 23.3 and 22.0; 16 of 25 over 512 to 131072, 14 heads on 2,
+// 110 and 115; 4 of 40 over 65536, 16 heads on 4, 120 and 127.  The rule goes by N, as the
+// counts are on the device: where trees have 128 rows or fewer in blocks of more, the second
+// group has nothing to do (64 blocks of 64 over 4000 with 30 nodes each, 32 heads on 8: 277 and
+// 199 at D = 128, 213 and 144 at D = 64).
 int groups_for(bool tree, int64_t N, int64_t G, int D) { return tree && D <= 128 && N * G > kRows ? 2 : 1; }
 
 // CTAs of a call: as many as run at once on the device.
