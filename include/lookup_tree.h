@@ -111,6 +111,12 @@ int lookup_norm_append(const void *q, const int64_t *q_strides, const void *k, c
  * block it reaches no others, and as the weighted sum has it (an infinity stays one); in a
  * slot before the block that `window` hides from some tokens and not from others it may
  * reach those.
+ * The weights are rounded to `type` for their product with v, as lookup_paged_attention's
+ * (relative 2^-8 for bfloat16; 2^-11 for float16, where those below 2^-21 of the largest
+ * are off by up to 2^-32 of it): the tensor cores take both operands in the cache's type.
+ * lse takes them before that; scores, maxima, sums and the weighted sum are float32, and out
+ * is rounded once.  A call whose bounded waits run out on the device returns NaN in every
+ * element of out and lse.
  * For a given request, N, D and head counts the sums are added in an order that depends
  * on the whole batch's lengths: the same call gives the same bits every time.
  * Blocks of more than 128 rows (N * Hq / Hkv) of D = 64 or 128 go through the cache once
