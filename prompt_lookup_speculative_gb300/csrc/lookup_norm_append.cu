@@ -10,9 +10,9 @@
 // What bounds it: the bytes of q, k and v, read once and written once.  The norm needs the
 // whole head before its first element can be written, so the head stays in registers:
 // a thread holds a unit of 16 elements (for a rotated unit, 8 pairs that share 8
-// angles) of kHeads heads, the D / 16 threads of a head are neighbours in a warp, and
+// angles) of one or two heads, the D / 16 threads of a head are neighbours in a warp, and
 // the sum of squares is exchanged by shuffles.  The angles and weights are read once
-// for the kHeads heads.
+// for a thread's heads.
 //
 // A head that is no power of two of units (D = 80, 96), a rotated part that is no multiple
 // of 16 elements, and strides or addresses that are no multiples of 16 bytes take a
@@ -36,11 +36,12 @@ using lkd::launch_pdl;
 using lkd::wait_for_prerequisite_grid;
 
 constexpr int kThreads = 256;
-// Heads of a thread, and CTAs per SM that its registers allow.  4 prompts of 8191 tokens, 32
-// and 8 heads of 128: 270 us with two heads and two CTAs, 254 and 334 with three and four;
-// with one head 265, 233 and 353 with three, four and five (3.3 TB/s at best, 49% of a copy's
-// rate).  64 trees of up to 63 nodes, 14 and 2 heads of 64, lose by it: 9.4 us, not 8.4.
-constexpr int kHeads = 1, kCtas = 4;
+// CTAs per SM for a thread's heads.  4 prompts of 8191 tokens, 32 and 8 heads of 128: 270 us
+// with two heads and two CTAs, 254 and 334 with three and four; with one head 265, 233 and 353
+// with three, four and five.  (Three CTAs of two heads: 68 us for 62, where 4 prompts have 14
+// and 2 heads of 64.)
+constexpr int ctas_for(int heads) { return heads == 2 ? 2 : 4; }
+constexpr int kFewTokens = 608;          // four for each of 152 SMs
 constexpr int kMaxD = 1024;
 
 struct Strides {
@@ -142,10 +143,19 @@ __device__ inline uint4 pack8(const float *x) {
     return make_uint4(pack2(x[0], x[1], T()), pack2(x[2], x[3], T()), pack2(x[4], x[5], T()), pack2(x[6], x[7], T()));
 }
 
+// A pair turned.  Which product each sum takes unrounded is spelled out (as the append without
+// a norm has it, but for bfloat16 in neighbours), so that a token's bits do not depend on how many
+// come with it.
+__device__ inline void turn(float &a, float &b, float c, float s) {
+    const float x = a, y = b;
+    a = fmaf(x, c, -(y * s));
+    b = fmaf(x, s, y * c);
+}
+
 // A thread's 16 elements of a head are x[0 .. 8) and x[8 .. 16), from its elements e0 and
 // e1 on.  Halves: x[j] pairs with x[8 + j].  Interleaved: x[2 j] with x[2 j + 1].
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads, kCtas) units_kernel(const __grid_constant__ Params p) {
+template <typename T, bool INTER, int kHeads>
+__global__ void __launch_bounds__(kThreads, ctas_for(kHeads)) units_kernel(const __grid_constant__ Params p) {
     wait_for_prerequisite_grid();
     allow_dependent_launch();
     if (int(blockIdx.x) >= p.grid) return report(p);
@@ -238,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) units_kernel(const __grid_con
                 unpack8<T>(v0[k], a);
                 unpack8<T>(v1[k], a + 8);
                 if (weight) {
-                    const float r = rsqrtf(sum[k] * inv_d + p.eps);
+                    const float r = rsqrtf(fmaf(sum[k], inv_d, p.eps));
 #pragma unroll
                     for (int j = 0; j < 16; ++j) a[j] *= r * w[j];
                 }
@@ -246,9 +256,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) units_kernel(const __grid_con
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         float &f = a[INTER ? 2 * j : j], &h = a[INTER ? 2 * j + 1 : 8 + j];
-                        const float f0 = f, h0_ = h;
-                        f = f0 * c[j] - h0_ * s[j];
-                        h = h0_ * c[j] + f0 * s[j];
+                        turn(f, h, c[j], s[j]);
                     }
                 }
                 v0[k] = pack8<T>(a);
@@ -319,14 +327,36 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
     for (int e = lane; e < half; e += 32) {
         const int j0 = p.interleaved ? 2 * e : e, j1 = p.interleaved ? 2 * e + 1 : e + half;
         const float *row = p.rotary + spot.angle * p.rot;
-        const float c = row[e], s = row[half + e], x = scaled(j0), y = scaled(j1);
-        from_f32(x * c - y * s, dst[j0]);
-        from_f32(y * c + x * s, dst[j1]);
+        const float c = row[e], s = row[half + e];
+        float x = scaled(j0), y = scaled(j1);
+        turn(x, y, c, s);
+        from_f32(x, dst[j0]);
+        from_f32(y, dst[j1]);
     }
     for (int j = 2 * half + lane; j < p.D; j += 32) {
         if (weight) from_f32(scaled(j), dst[j]);
         else dst[j] = src[j];
     }
+}
+
+// Heads of a thread of units_kernel, for `per` threads a token with one.  Many tokens: two of up
+// to 64 elements share what their thread reads and works out (us, two and one: 64 trees of 63,
+// 14 and 2 heads of 64, 7.6 and 8.8; 1024 of 64 116 and 119; 4 prompts of 8191 62 and 66; 14 and
+// 2 of 32 34 and 35; but 16 and 16 of 64 145 and 143), larger ones want the warps more (32 and 8
+// heads of 128, the same batches: 32.8 and 31.8, 530 and 468, 287 and 256; 16 and 4 of 256: 34
+// and 33, 545 and 479, 291 and 259).  Few tokens, all at once on the device: one head, the
+// shorter way (one tree of 15, 14 and 2 heads of 64: 3.4 and 2.8; 8 of 32: 3.6 and 3.0), unless a
+// CTA would have to go round twice for a token (32 and 8 heads of 128: 2.8 and 3.8; 3.2 and 4.4;
+// 512 single tokens 5.4 and 5.9; 504 with 64 and 8 heads 8.7 and 8.5).
+int heads_for(int64_t tokens, int64_t per, int D) {
+    if (tokens <= kFewTokens) return per > kThreads ? 2 : 1;
+    return D <= 64 ? 2 : 1;
+}
+
+template <typename T>
+auto units_for(bool interleaved, int heads) {
+    if (heads == 2) return interleaved ? units_kernel<T, true, 2> : units_kernel<T, false, 2>;
+    return interleaved ? units_kernel<T, true, 1> : units_kernel<T, false, 1>;
 }
 
 bool misaligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
@@ -381,9 +411,12 @@ int lookup_norm_append(const void *q, const int64_t *q_strides, const void *k, c
                           static_cast<const void *>(out_q), static_cast<const void *>(rotary), q_weight, k_weight})
         units = units && !misaligned(x, 16);
     int64_t grid = 0;
+    int each = 1;                                        // heads of a thread of units_kernel
     if (q || k) {
         if (units) {
-            const int64_t groups = (q ? (int64_t(Hq) + kHeads - 1) / kHeads : 0) + (k ? 2 * ((int64_t(Hkv) + kHeads - 1) / kHeads) : 0);
+            const int64_t heads = (q ? int64_t(Hq) : 0) + (k ? 2 * int64_t(Hkv) : 0);
+            each = heads_for(int64_t(B) * N, heads * (D / 16), D);
+            const int64_t groups = (q ? (int64_t(Hq) + each - 1) / each : 0) + (k ? 2 * ((int64_t(Hkv) + each - 1) / each) : 0);
             const int64_t per = groups * (D / 16);       // threads of a token
             if (per > INT32_MAX / kThreads) return LOOKUP_DRAFT_EINVAL;
             p.tokens = per < kThreads ? int32_t(kThreads / per) : 1;
@@ -399,9 +432,8 @@ int lookup_norm_append(const void *q, const int64_t *q_strides, const void *k, c
     if (all == 0) return LOOKUP_DRAFT_OK;
     p.grid = int32_t(grid);
     const bool half = type == LOOKUP_TYPE_F16;
-    auto kernel = units ? (interleaved ? (half ? units_kernel<__half, true> : units_kernel<__nv_bfloat16, true>)
-                                       : (half ? units_kernel<__half, false> : units_kernel<__nv_bfloat16, false>))
-                        : (half ? heads_kernel<__half> : heads_kernel<__nv_bfloat16>);
+    auto kernel = !units ? (half ? heads_kernel<__half> : heads_kernel<__nv_bfloat16>)
+                         : half ? units_for<__half>(interleaved, each) : units_for<__nv_bfloat16>(interleaved, each);
     return launch_pdl(kernel, unsigned(all), unsigned(kThreads), stream, p);
 }
 

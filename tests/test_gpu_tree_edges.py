@@ -11,7 +11,7 @@ pkg = pytest.importorskip("prompt_lookup_speculative_gb300")
 
 import tree_reference as ref  # noqa: E402
 from test_gpu_target import BF16, F16, close, gen  # noqa: E402
-from test_gpu_tree import tree_case  # noqa: E402
+from test_gpu_tree import check_norm, norm_case, tree_case  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,31 @@ def test_cached_values_that_are_not_finite_reach_all_that_see_them(N, Hq, Hkv, D
     got[..., [9, 33]] = want[0][..., [9, 33]]
     close(got, want[0], want[2], "out")
     close(lse, want[1], want[3], "lse")
+
+
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,rot,inter,pad", [
+    (10, 63, 7, 1, 64, 64, False, 0), (12, 55, 5, 3, 32, 16, True, 0), (40, 17, 1, 1, 16, 16, False, 8),
+    (9, 70, 7, 3, 128, 64, True, 0), (2, 5, 33, 7, 128, 128, False, 16), (1, 7, 16, 16, 256, 256, True, 0),
+    (3, 4, 70, 3, 64, 32, False, 0), (700, 1, 3, 1, 64, 64, True, 0),
+])
+def test_norm_append_of_few_and_many_tokens(dt, B, N, Hq, Hkv, D, rot, inter, pad):
+    """One and two heads of a thread, even and odd numbers of them, tokens that fill a CTA and those
+    that one CTA goes round for."""
+    lens = [(37 * r + 3) % 70 if r else 0 for r in range(B)]
+    qn = [(N + r) % (N + 1) if r % 5 == 1 else N for r in range(B)]
+    c = norm_case(B, N, Hq, Hkv, D, rot, 16, lens, qn, dt, B * N + D, pad)
+    whole, cached = check_norm(c, inter)
+    one = {n: x[:1] if n in ("q", "k", "v", "kv", "ql", "table", "depth") else x for n, x in c.items()}
+    q, to = check_norm(one, inter)                           # a token's bits are its own
+    assert torch.equal(q, whole[:1])
+    for j in range(-(-N // 16)):
+        page, rows = int(c["table"][0, j]), min(16, N - 16 * j)
+        assert torch.equal(to["kc"][page, :, :rows], cached["kc"][page, :, :rows])
+    q, to = check_norm(c | dict(qw=None, kw=None, depth=None), inter)
+    kc, vc = c["kc"].cuda(), c["vc"].cuda()
+    want, _ = pkg.lookup_kv_append(c["q"].cuda(), c["k"].cuda(), c["v"].cuda(), to["kv"], to["table"], kc, vc,
+                                   rotary=to["rotary"], q_len=to["ql"], interleaved=inter)
+    if not (inter and dt == BF16):
+        assert torch.equal(q, want) and torch.equal(to["kc"], kc)
+    assert torch.equal(to["vc"], vc)
