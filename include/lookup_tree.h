@@ -77,6 +77,9 @@ int lookup_tree_merge(const int32_t *root, const int32_t *chains, const int32_t 
  * The rest, N's range included, is lookup_kv_append's.  A head x of D elements becomes
  * x_j * w_j / sqrt(mean(x^2) + eps), then its pairs are rotated; everything in float32
  * (the sum of squares too), rounded once.  v is copied.
+ * Made for D a power of two from 16 to 512, a rotated part that is a multiple of 16 elements
+ * and addresses and strides that are multiples of 16 bytes; anything else is right, and takes
+ * three to four times as long.
  * status        int32 [B] or NULL: 1 when a token of the request has no slot or its
  *               rotated position is negative or past max_pos: that token is not cached
  *               and its row of out_q is zeros

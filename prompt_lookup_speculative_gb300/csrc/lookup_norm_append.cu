@@ -7,16 +7,20 @@
 // its pairs are turned, a' = a cos - b sin, b' = b cos + a sin.  Everything in float32;
 // the one rounding is the result's, to the tensors' type.
 //
-// What bounds it: the bytes of q, k and v, read once and written once.  The norm needs the
-// whole head before its first element can be written, so the head stays in registers:
-// a thread holds a unit of 16 elements (for a rotated unit, 8 pairs that share 8
-// angles) of one or two heads, the D / 16 threads of a head are neighbours in a warp, and
-// the sum of squares is exchanged by shuffles.  The angles and weights are read once
-// for a thread's heads.
+// What bounds it: the bytes of q, k and v, read once and written once, and for larger heads the
+// instructions around them: 4 prompts of 8191 tokens, 32 and 8 heads of 128, take 231 us
+// (3.3 TB/s) with the issue slots 65% busy, half of a CTA empty in its second round of a token's
+// 384 threads, and 48 to 72 bytes of a thread's state spilled.  The norm needs the whole head
+// before its first element can be written, so the head stays in registers: a thread holds a unit
+// of 16 elements (for a rotated unit, 8 pairs that share 8 angles) of one or two heads, the
+// D / 16 threads of a head are neighbours in a warp, and the sum of squares is exchanged by
+// shuffles.  The angles and weights are read once for a thread's heads.
 //
 // A head that is no power of two of units (D = 80, 96), a rotated part that is no multiple
 // of 16 elements, and strides or addresses that are no multiples of 16 bytes take a
-// kernel with a warp per head and a pair per lane and step: right for every case.
+// kernel with a warp per head and a pair per lane and step: right for every case, and slow, with
+// 2-byte accesses and every head read twice (those prompts with heads of 80: 688 us, and 597 with
+// 40 of 128 elements rotated; 64 trees of up to 63, 14 and 2 heads of 80: 31 us, of 64: 8.1).
 
 #include "lookup_draft.h"
 #include "lookup_tree.h"

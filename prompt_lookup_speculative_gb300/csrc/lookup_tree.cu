@@ -11,9 +11,10 @@
 // with l(c, c') > j, which made it.  So nothing is sequential: all l, then a sum over the
 // chains, then every position's node, then its ancestors.  Numbers from N on are left
 // out, and with them all that would hang on them, whose numbers are larger.
-// What bounds it: latency, a warp per request and its handful of dependent steps.  4096
-// requests with 16 chains of 8: 23.9 us; one with 2 of 7: 8.5 us as called, most of it the
-// enqueueing.
+// What bounds it: a warp's own instructions, 2700 for 16 chains of 8 (all pairs compared, every
+// position's first chain looked for, every node's ancestors gathered from its chain's start),
+// each waiting for the one before: the issue slots are 61% busy.  4096 such requests: 23.2 us, and
+// a copy of their bytes takes 1.1; one with 2 chains of 7: 3.4 us, 8.9 as called.
 
 #include "lookup_draft.h"
 #include "lookup_tree.h"
@@ -160,8 +161,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
 // sides rise; so a thread that takes the moves in their order for its own 16 bytes of
 // every row needs no copy and no barrier.
 // What bounds it: the moved rows' bytes, read and written once; all layers in one launch.
-// 64 requests, 32 layers with 8 heads of 128: 65 us as called for 71 MB, most of it what
-// the caller takes to list 64 tensors.
+// 64 requests, 32 layers with 8 heads of 128: 16.9 us for 71 MB (4.2 TB/s); 74 to 82 as called,
+// most of it what the caller takes to list 64 tensors.  30 moves each, all by one row: 85 us for
+// 503 MB (5.9 TB/s).  Four layers of one request: 2.4 us, 21 to 23 as called.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;            // moves in flight per thread
 constexpr int kMoveLayers = 128;         // of a launch
