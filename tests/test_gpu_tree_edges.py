@@ -146,3 +146,47 @@ def test_norm_append_of_few_and_many_tokens(dt, B, N, Hq, Hkv, D, rot, inter, pa
     if not (inter and dt == BF16):
         assert torch.equal(q, want) and torch.equal(to["kc"], kc)
     assert torch.equal(to["vc"], vc)
+
+
+def test_steps_of_a_loop_with_the_lookups_draft_as_one_chain():
+    """Draft, merge, greedy verification and append, step after step: what is committed is what the
+    target says, one token after the other, whatever the second chain proposes."""
+    B, K, V, N, steps = 5, 6, 40, 14, 6
+    g = gen(4)
+    follow = torch.randint(V, (V, V), generator=g)           # the target: a token from the last two
+    rows = []
+    for r in range(B):
+        x = torch.randint(V, (2,), generator=g).tolist()
+        while len(x) < 60 + 11 * r:
+            x.append(int(follow[x[-2], x[-1]]))
+        rows.append(x)
+    want = [list(x) for x in rows]
+    for x in want:
+        while len(x) < 400:
+            x.append(int(follow[x[-2], x[-1]]))
+    history = torch.tensor(sum(rows, []), dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0] + [len(x) for x in rows], dtype=torch.int64).cumsum(0).cuda()
+    most = 0
+    for step in range(steps):
+        draft, length, _, _ = pkg.lookup_draft_ex(history, offsets, 2, 8, K)
+        at = offsets.tolist()
+        now = [history[at[r]:at[r + 1]].tolist() for r in range(B)]
+        assert all(x == want[r][:len(x)] for r, x in enumerate(now))
+        other = torch.randint(V, (B, K), generator=g).to(torch.int32)
+        for r in range(0, B, 2):                             # a model that is right for a while
+            other[r, :3] = torch.tensor(want[r][len(now[r]):len(now[r]) + 3])
+        chains = torch.stack([draft, other.cuda()], 1)
+        lengths = torch.stack([length, torch.full_like(length, K)], 1)
+        root = torch.tensor([x[-1] for x in now], dtype=torch.int32, device="cuda")
+        tokens, parent, depth, mask, n = pkg.lookup_tree_merge(root, chains, lengths, N)
+        logits = torch.zeros((B, N, V))
+        t, p = tokens.tolist(), parent.tolist()
+        for r in range(B):
+            for i in range(int(n[r])):
+                before = t[r][p[r][i]] if i else now[r][-2]
+                logits[r, i, follow[before, t[r][i]]] = 9.0
+        acc, commit, ncommit, path, _ = pkg.lookup_verify_tree(tokens, parent, n, logits.cuda())
+        assert torch.equal(ncommit, acc + 1) and bool((acc.cpu()[::2] >= 3).all())
+        most = max(most, int(acc.max()))
+        history, offsets = pkg.lookup_append(history, offsets, commit, ncommit)
+    assert most >= 4                                         # (the lookup's: the target goes round)
